@@ -82,6 +82,23 @@ CUresult encode_tensor_map_3d_bf16(CUtensorMap* map, const void* base, uint64_t 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+CUresult encode_tensor_map_16(CUtensorMap* map, const void* base, bool fp16, int rank, const uint64_t* dims,
+                              const uint32_t* box) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return CUDA_ERROR_NOT_FOUND;
+  cuuint64_t gdim[4], strides[3], bytes = 2;
+  cuuint32_t b[4], estr[4] = {1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    gdim[i] = dims[i];
+    b[i] = box[i];
+    bytes *= dims[i];
+    if (i < rank - 1) strides[i] = bytes;
+  }
+  return fn(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+            const_cast<void*>(base), gdim, strides, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
 int device_sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 1;
@@ -246,6 +263,50 @@ int attn_common(const psa_bf16_t* q, const psa_bf16_t* k, const psa_bf16_t* v, c
   return cuda_status(e);
 }
 
+// ---- serving operators
+constexpr int kMaxCache = 1 << 20;    // entries of a cache or prefix (as many as the longest prefill)
+constexpr int kMaxDecodeTokens = 256; // new tokens per sequence
+
+struct Range {
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Range& a, const Range& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+}
+bool misaligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
+// Heads, head size and type shared by the serving operators.
+int check_serve(int B, int Hq, int Hkv, int d, int dtype) {
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || d <= 0) return PSA_ERR_ARG;
+  if (dtype != PSA_BF16 && dtype != PSA_FP16) return PSA_ERR_ARG;
+  if (d != 64 && d != 128) return PSA_ERR_UNSUPPORTED;
+  if (Hq % Hkv) return PSA_ERR_SHAPE;
+  if (static_cast<long long>(B) * Hq > (1 << 24)) return PSA_ERR_SHAPE;
+  return PSA_OK;
+}
+
+int check_decode_shape(int B, int Hq, int Hkv, int T, int d, int Bp, int P, int C) {
+  const int s = check_serve(B, Hq, Hkv, d, PSA_BF16);
+  if (s != PSA_OK) return s;
+  if (T <= 0 || Bp <= 0 || P < 0 || C < 0 || (P == 0 && C == 0)) return PSA_ERR_ARG;
+  if (T > kMaxDecodeTokens || P > kMaxCache || C > kMaxCache) return PSA_ERR_UNSUPPORTED;
+  if (B % Bp || static_cast<long long>(B) * Hq * T >= (1LL << 31)) return PSA_ERR_SHAPE;
+  return psa::decode_workspace_bytes(B, Hq / Hkv, Hkv, T, d, Bp, P, C) ? PSA_OK : PSA_ERR_SHAPE;
+}
+
+int check_evict_shape(int B, int Hkv, int C, int budget) {
+  if (B <= 0 || Hkv <= 0 || C <= 0 || budget <= 0) return PSA_ERR_ARG;
+  if (C > kMaxCache) return PSA_ERR_UNSUPPORTED;
+  if (budget > C || static_cast<long long>(B) * Hkv > (1 << 24) ||
+      static_cast<long long>(B) * Hkv * ((budget + 63) / 64) >= (1LL << 31))
+    return PSA_ERR_SHAPE;
+  return PSA_OK;
+}
+
+size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
 }  // namespace
 
 extern "C" {
@@ -261,11 +322,12 @@ const char* psa_status_string(int status) {
     case PSA_ERR_TIMEOUT: return "device: a bounded wait ran out and the kernel stopped";
     case PSA_ERR_CSR: return "device: a block list entry was out of range or repeated";
     case PSA_ERR_DEVICE: return "no sm_100 (B200) device is current, or a tensor lives on another device";
+    case PSA_ERR_LENGTH: return "device: a sequence length was out of range and was clamped";
     default: return "unknown status";
   }
 }
 
-int psa_version(void) { return 200; }
+int psa_version(void) { return 300; }
 
 size_t psa_workspace_size(int B, int H, int N, int d) {
   if (check_shape(B, H, N, d, kBlock) != PSA_OK) return 0;
@@ -498,6 +560,124 @@ int psa_read_fixup_count(const void* workspace, int* rerun, int* exact, void* st
   *rerun = v[0];
   *exact = v[1];
   return PSA_OK;
+}
+
+size_t psa_decode_workspace_size(int B, int Hq, int Hkv, int T, int d, int Bp, int P, int C) {
+  if (check_decode_shape(B, Hq, Hkv, T, d, Bp, P, C) != PSA_OK) return 0;
+  return psa::decode_workspace_bytes(B, Hq / Hkv, Hkv, T, d, Bp, P, C);
+}
+
+int psa_decode(const void* q, const void* k_prefix, const void* v_prefix, const int* prefix_len,
+               const void* k_cache, const void* v_cache, const int* cache_len, int B, int Hq, int Hkv, int T, int d,
+               int Bp, int P, int C, int dtype, void* out, float* lse, void* workspace, size_t workspace_bytes,
+               void* stream) {
+  if (!q || !out || !workspace) return PSA_ERR_ARG;
+  int s = check_serve(B, Hq, Hkv, d, dtype);
+  if (s == PSA_OK) s = check_decode_shape(B, Hq, Hkv, T, d, Bp, P, C);
+  if (s != PSA_OK) return s;
+  if ((P > 0) != (k_prefix != nullptr) || (P > 0) != (v_prefix != nullptr) || (P == 0 && prefix_len) ||
+      (C > 0) != (k_cache != nullptr) || (C > 0) != (v_cache != nullptr) || (C == 0 && cache_len))
+    return PSA_ERR_ARG;
+  if (misaligned(q, 16) || misaligned(k_prefix, 16) || misaligned(v_prefix, 16) || misaligned(k_cache, 16) ||
+      misaligned(v_cache, 16) || misaligned(out, 16) || misaligned(lse, 4) || misaligned(prefix_len, 4) ||
+      misaligned(cache_len, 4) || misaligned(workspace, 256))
+    return PSA_ERR_ARG;
+  if (workspace_bytes < psa::decode_workspace_bytes(B, Hq / Hkv, Hkv, T, d, Bp, P, C)) return PSA_ERR_CAPACITY;
+  if ((s = check_device({q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, cache_len, out, lse, workspace})) !=
+      PSA_OK)
+    return s;
+  psa::DecodeLaunch a = {};
+  a.q = q;
+  a.k_prefix = k_prefix;
+  a.v_prefix = v_prefix;
+  a.prefix_len = prefix_len;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.cache_len = cache_len;
+  a.B = B;
+  a.G = Hq / Hkv;
+  a.Hkv = Hkv;
+  a.T = T;
+  a.d = d;
+  a.Bp = Bp;
+  a.P = P;
+  a.C = C;
+  a.fp16 = dtype == PSA_FP16;
+  a.out = out;
+  a.lse = lse;
+  a.ws = static_cast<char*>(workspace);
+  return cuda_status(psa::launch_decode(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t psa_cache_evict_workspace_size(int B, int Hkv, int C, int budget) {
+  if (check_evict_shape(B, Hkv, C, budget) != PSA_OK) return 0;
+  return 256 + round256(static_cast<size_t>(B) * 4) + round256(static_cast<size_t>(B) * Hkv * budget * 4);
+}
+
+int psa_cache_evict(const void* k, const void* v, const float* score, const int* pos, const int* cache_len, int B,
+                    int Hkv, int C, int d, int budget, int sink, int recent, int C_out, void* k_out, void* v_out,
+                    float* score_out, int* pos_out, int* len_out, int* kept, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  if (!k || !v || !score || !k_out || !v_out || !score_out || !pos_out || !len_out || !kept || !workspace)
+    return PSA_ERR_ARG;
+  int s = check_evict_shape(B, Hkv, C, budget);
+  if (s != PSA_OK) return s;
+  if (d <= 0 || sink < 0 || recent < 0 || static_cast<long long>(sink) + recent > budget) return PSA_ERR_ARG;
+  if (d != 64 && d != 128) return PSA_ERR_UNSUPPORTED;
+  if (C_out < budget || C_out > kMaxCache) return PSA_ERR_SHAPE;
+  if (misaligned(k, 16) || misaligned(v, 16) || misaligned(k_out, 16) || misaligned(v_out, 16) ||
+      misaligned(score, 4) || misaligned(pos, 4) || misaligned(cache_len, 4) || misaligned(score_out, 4) ||
+      misaligned(pos_out, 4) || misaligned(len_out, 4) || misaligned(kept, 4) || misaligned(workspace, 256))
+    return PSA_ERR_ARG;
+  // in place means all of it: the same buffers throughout; otherwise no
+  // output may overlap an input or another output
+  const bool in_place = k_out == k;
+  if (in_place && (v_out != v || score_out != score || (pos && pos_out != pos) || C_out != C)) return PSA_ERR_ARG;
+  const size_t heads = static_cast<size_t>(B) * Hkv, in = heads * C, o = heads * C_out;
+  const size_t need = psa_cache_evict_workspace_size(B, Hkv, C, budget);
+  if (workspace_bytes < need) return PSA_ERR_CAPACITY;
+  const Range ins[] = {{k, in * d * 2}, {v, in * d * 2}, {score, in * 4}, {pos, pos ? in * 4 : 0},
+                       {cache_len, cache_len ? static_cast<size_t>(B) * 4 : 0}};
+  const Range outs[] = {{k_out, o * d * 2},  {v_out, o * d * 2}, {score_out, o * 4},
+                        {pos_out, o * 4},    {len_out, static_cast<size_t>(B) * 4},
+                        {kept, heads * budget * 4}, {workspace, need}};
+  for (int i = 0; i < 7; ++i) {
+    for (int j = 0; j < 5; ++j) {
+      // each tensor over itself in place, and the lengths over themselves
+      if (i == j && (i == 4 || in_place) && outs[i].p == ins[j].p) continue;
+      if (overlap(outs[i], ins[j])) return PSA_ERR_ARG;
+    }
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], outs[j])) return PSA_ERR_ARG;
+  }
+  if ((s = check_device({k, v, score, pos, cache_len, k_out, v_out, score_out, pos_out, len_out, kept,
+                         workspace})) != PSA_OK)
+    return s;
+  char* ws = static_cast<char*>(workspace);
+  psa::EvictLaunch a = {};
+  a.k = k;
+  a.v = v;
+  a.score = score;
+  a.pos = pos;
+  a.cache_len = cache_len;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.C = C;
+  a.d = d;
+  a.budget = budget;
+  a.sink = sink;
+  a.recent = recent;
+  a.C_out = C_out;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.score_out = score_out;
+  a.pos_out = pos_out;
+  a.len_out = len_out;
+  a.kept = kept;
+  a.status = reinterpret_cast<int*>(ws);
+  a.nk = reinterpret_cast<int*>(ws + 256);
+  a.late = reinterpret_cast<int*>(ws + 256 + round256(static_cast<size_t>(B) * 4));
+  return cuda_status(psa::launch_evict(a, static_cast<cudaStream_t>(stream)));
 }
 
 int psa_read_status(const void* workspace, int* status, void* stream) {

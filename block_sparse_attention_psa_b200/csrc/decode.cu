@@ -1,0 +1,861 @@
+// decode.cu -- attention of a batch's new tokens over a prefix that groups
+// of sequences share and over each sequence's own cache, in one softmax:
+//   out_t = sum_j e^{s_tj} v_j / sum_j e^{s_tj},  s = q.k / sqrt(d)
+// over the visible prefix keys and cache slots.  The largest exponent, the
+// sum and the weighted values of disjoint key sets combine exactly, so the
+// keys are cut wherever the machine wants them cut (decode_kernel) and the
+// parts joined afterwards (merge_kernel).
+//
+// Work is bound by reading K and V once at few rows per key (4 d rows
+// operations against 4 d bytes), by the exponentials and the tensor cores at
+// many.
+//  * Rows.  All rows that read the same K and V share one pass over them: the
+//    G query heads of a KV head, the T new tokens and, for the prefix, the
+//    sequences of the group.  A row tile is up to 128 of them, the M of the
+//    products S = Q K^T (Q, K in shared memory) and O += P V (P in TMEM,
+//    written over S; V MN-major in shared memory).  An unfilled tile costs
+//    tensor time, which few rows leave idle.
+//  * Streams.  A CTA runs two softmax warpgroups, each with its own S/P and O
+//    in TMEM (512 columns in all).  With two row tiles or more each takes one
+//    of a pair, so that K and V are read once for 256 rows; with one row tile
+//    they take alternate key tiles and give two parts.  Items go to the
+//    streams in turn, one thread issues every product: PV of the item two
+//    back, then S of this one, so that one stream's softmax covers the other's
+//    products.
+//  * Split.  The key tiles of all units (KV head x row-tile pair) are laid
+//    out in one line, the prefixes first, and cut into equal runs, one per
+//    SM: every SM reads the same number of tiles whatever the lengths, which
+//    live on the device.  A unit's run in one CTA is a piece; its parts
+//    (running maximum, sum and unnormalised O, fp32) go to the workspace.
+//  * Stabiliser.  A row's reference exponent only moves when a tile's maximum
+//    passes it by 2^8, so O is rarely rescaled, and terms stay below 2^8.
+//  * Rounding.  P is rounded to the inputs' type for the tensor core (half a
+//    step, 2^-9 of the term in bf16), sums, O and the parts stay in fp32, the
+//    output is rounded once.
+//  * V rows past a sequence's length are cleared in shared memory before the
+//    product (0 x NaN would reach the sum); K rows past it only touch columns
+//    that are masked.
+// Every wait is bounded.
+#include "internal.h"
+#include "sm100.cuh"
+
+namespace psa {
+namespace {
+
+constexpr int kThreads = 384;      // WG0: Q/K loads, MMA issue, V loads; WG1, WG2: softmax streams
+constexpr int kRegsProducer = 72;  // 128 x 72 + 256 x 216 = 384 x 168
+constexpr int kRegsSoftmax = 216;
+constexpr int kMaxCtas = 256;      // upper bound of the grid the workspace is sized for
+constexpr int kRing = 4;           // pieces in flight between the scheduler and its readers
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescale = 8.0f;   // log2 units the reference may lag behind the maximum
+
+template <int D>
+struct Cfg {
+  static constexpr int kChunks = D / 64;        // 128-byte column chunks
+  static constexpr int kTile = 128 * D * 2;     // 128 rows
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kOffQ = 0;               // two row tiles
+  static constexpr int kOffK = 2 * kTile;
+  static constexpr int kOffV = kOffK + kStages * kTile;
+  static constexpr int kOffMisc = kOffV + kStages * kTile;
+  static constexpr int kSmem = kOffMisc + 1024 + 1024;  // + alignment slack
+  static_assert(kSmem <= 232448, "shared memory of one CTA");
+};
+
+struct Params {
+  const int* prefix_len;
+  const int* cache_len;
+  int B, G, Hkv, T, Bp, n, P, C;
+  int GT;              // rows of one sequence and KV head
+  int nseg;            // prefixes (if any), then caches (if any)
+  int npre;            // prefixes among them
+  int pre_nb, pre_rb;  // prefix row tile: sequences x rows of each
+  int pre_rt, pre_up;  // row tiles and units (pairs) per (prefix, KV head)
+  int own_rb, own_rt, own_up;
+  float scale_log2;
+  long long pre_slots; // slots of the prefix region: the caches' parts start behind it
+  long long* seg_off;  // [nseg + 1] first tile of each segment
+  float* part_o;       // parts: rows x d
+  float2* part_ml;     // reference (log2 units), sum
+  int* status;
+};
+
+// A piece: part of one unit's key tiles, as the scheduler publishes it.
+struct Piece {
+  int prefix;     // 1: a prefix, 0: a cache
+  int outer, hkv; // prefix or sequence, KV head
+  int tile0;      // first row tile
+  int pair;       // 1: both streams read every key tile, for two row tiles
+  int j0, nt;     // key tiles
+  int len;        // valid keys of the segment
+  int slot;       // unit + CTA within the region: the place of its parts
+  int tiles, items, qpos;  // running counts of this CTA at the piece's start
+};
+constexpr int kPieceInts = sizeof(Piece) / 4;
+
+__device__ __forceinline__ int seg_len(const Params& p, int s) {
+  if (s < p.npre) return min(max(p.prefix_len ? __ldg(p.prefix_len + s) : p.P, 0), p.P);
+  return min(max(p.cache_len ? __ldg(p.cache_len + s - p.npre) : p.C, 0), p.C);
+}
+__device__ __forceinline__ bool seg_bad(const Params& p, int s) {
+  if (s < p.npre) return p.prefix_len && (p.prefix_len[s] < 0 || p.prefix_len[s] > p.P);
+  return p.cache_len && (p.cache_len[s - p.npre] < 0 || p.cache_len[s - p.npre] > p.C);
+}
+__device__ __forceinline__ int seg_units(const Params& p, int s) { return p.Hkv * (s < p.npre ? p.pre_up : p.own_up); }
+
+__device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (clock64() - t0 > kWaitCycles) return;
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void reg_dealloc() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_alloc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+
+template <int D, bool FP16>
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_kernel(const __grid_constant__ CUtensorMap tmQp, const __grid_constant__ CUtensorMap tmQc,
+                  const __grid_constant__ CUtensorMap tmKp, const __grid_constant__ CUtensorMap tmVp,
+                  const __grid_constant__ CUtensorMap tmKc, const __grid_constant__ CUtensorMap tmVc, const Params p) {
+  using C = Cfg<D>;
+  constexpr int kSt = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem + C::kOffQ;
+  uint8_t* sK = smem + C::kOffK;
+  uint8_t* sV = smem + C::kOffV;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffMisc);
+  uint64_t* q_full = bars + 0;    // [2] a row tile landed              (TMA)
+  uint64_t* q_empty = bars + 2;   // [2] its last S product done        (commit)
+  uint64_t* k_full = bars + 4;    // [kSt]
+  uint64_t* k_empty = bars + 8;   // [kSt] last S product of the tile   (commit)
+  uint64_t* v_full = bars + 12;   // [kSt]
+  uint64_t* v_empty = bars + 16;  // [kSt] last PV product of the tile  (commit)
+  uint64_t* s_full = bars + 20;   // [2] S of the stream ready          (commit)
+  uint64_t* p_full = bars + 22;   // [2] P written over it              (4 warps)
+  uint64_t* o_full = bars + 24;   // [2] last PV of the piece done      (commit)
+  uint64_t* pc_full = bars + 26;  // [kRing] a piece published
+  uint64_t* pc_empty = bars + 30; // [kRing] read by V loads, MMA issue, 8 softmax warps
+  uint64_t* drain = bars + 34;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc + 288);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* start_seg = reinterpret_cast<int*>(tmem_slot + 2);
+  long long* start_off = reinterpret_cast<long long*>(smem + C::kOffMisc + 304);  // first tile of start_seg
+  long long* red = start_off + 1;                                                 // [12 + 1]
+  volatile int* ring = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 512); // [kRing][kPieceInts]
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1);
+    }
+    for (int i = 0; i < kSt; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&pc_full[i], 1);
+      mbar_init(&pc_empty[i], 10);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *start_seg = p.nseg;
+    *start_off = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (warp == 2 && lane == 0) {
+    tma_prefetch_desc(&tmKp);
+    tma_prefetch_desc(&tmVp);
+    tma_prefetch_desc(&tmKc);
+    tma_prefetch_desc(&tmVc);
+    tma_prefetch_desc(&tmQp);
+    tma_prefetch_desc(&tmQc);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  grid_dep_launch();
+  grid_dep_wait();
+
+  // ---- schedule: total tiles, then the segment in which this CTA's run starts
+  long long mine = 0;
+  bool bad = false;
+  for (int s = threadIdx.x; s < p.nseg; s += kThreads) {
+    mine += static_cast<long long>((seg_len(p, s) + 127) / 128) * seg_units(p, s);
+    bad |= blockIdx.x == 0 && seg_bad(p, s);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) red[warp] = mine;
+  bad = __syncthreads_or(bad);
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) total += red[w];
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *p.status = bad ? kStatusLength : 0;  // the call's first write of the status word
+    p.seg_off[p.nseg] = total;
+  }
+  const long long x0 = total * blockIdx.x / gridDim.x, x1 = total * (blockIdx.x + 1) / gridDim.x;
+  if (x0 < x1 || blockIdx.x == 0) {
+    long long run = 0;
+    for (int s0 = 0; s0 < p.nseg; s0 += kThreads) {
+      const int s = s0 + threadIdx.x;
+      const long long t =
+          s < p.nseg ? static_cast<long long>((seg_len(p, s) + 127) / 128) * seg_units(p, s) : 0;
+      long long inc = t;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+      }
+      __syncthreads();
+      if (lane == 31) red[warp] = inc;
+      __syncthreads();
+      long long base = run;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        base += w < warp ? red[w] : 0;
+        run += red[w];
+      }
+      const long long lo = base + inc - t, hi = base + inc;
+      if (lo <= x0 && x0 < hi) {
+        *start_seg = s;
+        *start_off = lo;
+      }
+      if (blockIdx.x == 0 && s < p.nseg) p.seg_off[s] = lo;
+    }
+  }
+  __syncthreads();
+
+  if (warp < 4) {
+    reg_dealloc<kRegsProducer>();
+    if (warp == 0) {
+      // ---------------------------------------------------- scheduler, Q and K loads
+      long long x = x0, off = *start_off;
+      int s = *start_seg;
+      int tiles = 0, items = 0, qpos = 0, np = 0, kl = 0, ql = 0;
+      bool ok = true;
+      int lens = 0, lens0 = -64;  // lane l holds the length of segment lens0 + l
+      while (ok && x < x1) {
+        if (s - lens0 >= 32) {
+          lens0 = s;
+          lens = s + lane < p.nseg ? seg_len(p, s + lane) : 0;
+        }
+        const int len = __shfl_sync(0xffffffffu, lens, s - lens0);
+        const int nkt = (len + 127) / 128;
+        const long long here = static_cast<long long>(nkt) * seg_units(p, s);
+        if (x >= off + here) {
+          off += here;
+          ++s;
+          continue;
+        }
+        Piece c;
+        const int lu = static_cast<int>((x - off) / nkt);
+        c.prefix = s < p.npre;
+        c.outer = c.prefix ? s : s - p.npre;
+        const int up = c.prefix ? p.pre_up : p.own_up, rt = c.prefix ? p.pre_rt : p.own_rt;
+        c.hkv = lu / up;
+        c.tile0 = 2 * (lu - c.hkv * up);
+        c.pair = c.tile0 + 1 < rt;
+        c.j0 = static_cast<int>(x - off - static_cast<long long>(lu) * nkt);
+        c.nt = static_cast<int>(min(static_cast<long long>(nkt - c.j0), x1 - x));
+        c.len = len;
+        c.slot = c.outer * p.Hkv * up + lu + static_cast<int>(blockIdx.x);
+        c.tiles = tiles;
+        c.items = items;
+        c.qpos = qpos;
+        if (lane == 0) {
+          const int slot = np % kRing;
+          if (np >= kRing) ok = mbar_wait(&pc_empty[slot], ((np / kRing) - 1) & 1, abort_flag, p.status);
+          if (ok) {
+            const int* w = reinterpret_cast<const int*>(&c);
+            for (int i = 0; i < kPieceInts; ++i) ring[slot * kPieceInts + i] = w[i];
+            mbar_arrive(&pc_full[slot]);
+          }
+          // Q
+          const CUtensorMap* mq = c.prefix ? &tmQp : &tmQc;
+          for (int i = 0; i <= c.pair && ok; ++i) {
+            const int qs = (qpos + i) & 1, n = (qpos + i) >> 1;
+            ok = mbar_wait(&q_empty[qs], (n & 1) ^ 1, abort_flag, p.status);
+            if (!ok) break;
+            const int tile = c.tile0 + i;
+            int r = 0, b;
+            uint32_t rows;
+            if (c.prefix) {
+              if (p.GT >= 128) {
+                const int per = (p.GT + 127) / 128;
+                b = c.outer * p.n + tile / per;
+                r = tile % per * 128;
+              } else {
+                b = c.outer * p.n + tile * p.pre_nb;
+              }
+              rows = static_cast<uint32_t>(p.pre_nb * p.pre_rb);
+            } else {
+              b = c.outer;
+              r = tile * 128;
+              rows = static_cast<uint32_t>(p.own_rb);
+            }
+            mbar_arrive_expect_tx(&q_full[qs], rows * 128 * C::kChunks);
+#pragma unroll
+            for (int ch = 0; ch < C::kChunks; ++ch)
+              tma_load_4d(mq, sQ + qs * C::kTile + ch * 16384, &q_full[qs], 64 * ch, r, c.hkv, b);
+            ql = qpos + i + 1;
+          }
+          // K
+          const CUtensorMap* mk = c.prefix ? &tmKp : &tmKc;
+          for (int j = 0; j < c.nt && ok; ++j) {
+            const int st = (tiles + j) % kSt, n = (tiles + j) / kSt;
+            ok = mbar_wait(&k_empty[st], (n & 1) ^ 1, abort_flag, p.status);
+            if (!ok) break;
+            const int y = 128 * (c.j0 + j);
+            const int halves = c.len - y > 64 ? 2 : 1;
+            mbar_arrive_expect_tx(&k_full[st], halves * 64 * 128 * C::kChunks);
+            for (int h = 0; h < halves; ++h)
+#pragma unroll
+              for (int ch = 0; ch < C::kChunks; ++ch)
+                tma_load_3d(mk, sK + st * C::kTile + ch * 16384 + h * 8192, &k_full[st], 64 * ch, y + 64 * h,
+                            c.outer * p.Hkv + c.hkv);
+            kl = tiles + j + 1;
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        tiles += c.nt;
+        items += c.pair ? 2 * c.nt : c.nt;
+        qpos += 1 + c.pair;
+        x += c.nt;
+        ++np;
+      }
+      if (lane == 0) {
+        // the end mark: a piece without tiles
+        const int slot = np % kRing;
+        if (ok && np >= kRing) ok = mbar_wait(&pc_empty[slot], ((np / kRing) - 1) & 1, abort_flag, p.status);
+        if (ok) {
+          for (int i = 0; i < kPieceInts; ++i) ring[slot * kPieceInts + i] = 0;
+          mbar_arrive(&pc_full[slot]);
+        }
+        // no bulk copy may still be writing shared memory when the CTA leaves
+        for (int t = max(0, kl - kSt); t < kl; ++t) mbar_drain(&k_full[t % kSt], (t / kSt) & 1);
+        for (int t = max(0, ql - 2); t < ql; ++t) mbar_drain(&q_full[t & 1], (t >> 1) & 1);
+      }
+      __syncwarp();
+    } else if (lane == 0 && (warp == 1 || warp == 2)) {
+      // reads the next piece; false at the end or on a timeout
+      int np = 0;
+      auto next = [&](Piece& c) -> bool {
+        const int slot = np % kRing;
+        if (!mbar_wait(&pc_full[slot], (np / kRing) & 1, abort_flag, p.status)) return false;
+        int* w = reinterpret_cast<int*>(&c);
+        for (int i = 0; i < kPieceInts; ++i) w[i] = ring[slot * kPieceInts + i];
+        mbar_arrive(&pc_empty[slot]);
+        ++np;
+        return c.nt > 0;
+      };
+      if (warp == 2) {
+        // -------------------------------------------------- V loads
+        Piece c;
+        int vl = 0;
+        bool ok = true;
+        while (ok && next(c)) {
+          const CUtensorMap* mv = c.prefix ? &tmVp : &tmVc;
+          for (int j = 0; j < c.nt; ++j) {
+            const int st = (c.tiles + j) % kSt, n = (c.tiles + j) / kSt;
+            if (!(ok = mbar_wait(&v_empty[st], (n & 1) ^ 1, abort_flag, p.status))) break;
+            const int y = 128 * (c.j0 + j);
+            const int halves = c.len - y > 64 ? 2 : 1;
+            mbar_arrive_expect_tx(&v_full[st], halves * 64 * 128 * C::kChunks);
+            for (int h = 0; h < halves; ++h)
+#pragma unroll
+              for (int ch = 0; ch < C::kChunks; ++ch)
+                tma_load_3d(mv, sV + st * C::kTile + ch * 16384 + h * 8192, &v_full[st], 64 * ch, y + 64 * h,
+                            c.outer * p.Hkv + c.hkv);
+            vl = c.tiles + j + 1;
+          }
+        }
+        for (int t = max(0, vl - kSt); t < vl; ++t) mbar_drain(&v_full[t % kSt], (t / kSt) & 1);
+      } else {
+        // -------------------------------------------------- MMA issue
+        constexpr uint32_t kIdescS = idesc_f16_f32(FP16, 128, 128, 0, 0);
+        constexpr uint32_t kIdescO = idesc_f16_f32(FP16, 128, D, 0, 1);
+        const uint64_t dQ0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
+        const uint64_t dK0 = sdesc_sw128(smem_u32(sK), 16, 1024);
+        // V is read MN-major: 64-feature atoms 16 KB apart (d = 64: one atom)
+        const uint64_t dV0 = sdesc_sw128(smem_u32(sV), D == 128 ? 16384 : 0, 1024);
+        constexpr uint64_t kStep = C::kTile >> 4;
+        int cnt = 0;                   // items issued
+        int pv_tile[2] = {-1, -1};     // the PV product due on each stream: its tile,
+        uint32_t pv_flags[2] = {0, 0}; // 1: adds to O, 2: last of its tile, 4: last of its piece
+        int pv_n[2] = {0, 0};
+        bool ok = true;
+        auto issue_pv = [&](int s) -> bool {
+          const int t = s ? pv_tile[1] : pv_tile[0];
+          if (t < 0) return true;
+          const uint32_t f = s ? pv_flags[1] : pv_flags[0];
+          const int n = s ? pv_n[1] : pv_n[0];
+          const int st = t % kSt;
+          if (!mbar_wait(&p_full[s], n & 1, abort_flag, p.status)) return false;
+          if (!mbar_wait(&v_full[st], (t / kSt) & 1, abort_flag, p.status)) return false;
+          tc_fence_after();
+          const uint32_t a = tbase + 128 * s, o = tbase + 256 + D * s;
+          const uint64_t b = dV0 + st * kStep;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc_mma_f16_ts(o, a + 8 * kk, b + 128 * kk, kIdescO, kk ? 1u : (f & 1u));
+          if (f & 2u) tc_commit(&v_empty[st]);
+          if (f & 4u) tc_commit(&o_full[s]);
+          if (s) {
+            ++pv_n[1];
+            pv_tile[1] = -1;
+          } else {
+            ++pv_n[0];
+            pv_tile[0] = -1;
+          }
+          return true;
+        };
+        Piece c;
+        while (ok && next(c)) {
+          const int ni = c.pair ? 2 * c.nt : c.nt;
+          for (int i = 0; i < ni; ++i, ++cnt) {
+            const int s = cnt & 1;
+            const int j = c.pair ? i >> 1 : i;
+            const int t = c.tiles + j, st = t % kSt;
+            const int q = c.qpos + (c.pair ? (i & 1) : 0), qs = q & 1;
+            if (!(ok = issue_pv(s))) break;
+            if (i <= c.pair && !(ok = mbar_wait(&q_full[qs], (q >> 1) & 1, abort_flag, p.status))) break;
+            if (!(ok = mbar_wait(&k_full[st], (t / kSt) & 1, abort_flag, p.status))) break;
+            tc_fence_after();
+            const uint64_t a = dQ0 + qs * kStep, b = dK0 + st * kStep;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc_mma_bf16(tbase + 128 * s, a + (kk >> 2) * 1024 + (kk & 3) * 2, b + (kk >> 2) * 1024 + (kk & 3) * 2,
+                          kIdescS, kk ? 1u : 0u);
+            tc_commit(&s_full[s]);
+            const bool tile_end = !c.pair || (i & 1);
+            if (tile_end) tc_commit(&k_empty[st]);
+            if (i >= ni - 1 - c.pair) tc_commit(&q_empty[qs]);
+            const uint32_t f = (i >= 2 ? 1u : 0u) | (tile_end ? 2u : 0u) | (i >= ni - 2 ? 4u : 0u);
+            if (s) {
+              pv_tile[1] = t;
+              pv_flags[1] = f;
+            } else {
+              pv_tile[0] = t;
+              pv_flags[0] = f;
+            }
+          }
+        }
+        if (ok) ok = issue_pv(cnt & 1);
+        if (ok) ok = issue_pv((cnt & 1) ^ 1);
+        // every product must be done before TMEM is freed
+        tc_commit(drain);
+        mbar_drain(drain, 0);
+      }
+    }
+    __syncwarp();
+  } else {
+    reg_alloc<kRegsSoftmax>();
+    // -------------------------------------------------------- softmax streams
+    const int s = (warp >> 2) - 1;
+    const int x = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
+    const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tbase + lane_addr + 128 * s;
+    const uint32_t o_addr = tbase + lane_addr + 256 + D * s;
+    int np = 0, ns = 0, no = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status));
+    };
+    while (ok) {
+      const int slot = np % kRing;
+      if (!(ok = wait(&pc_full[slot], (np / kRing) & 1))) break;
+      Piece c;
+      {
+        int* w = reinterpret_cast<int*>(&c);
+#pragma unroll
+        for (int i = 0; i < kPieceInts; ++i) w[i] = ring[slot * kPieceInts + i];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pc_empty[slot]);
+      ++np;
+      if (c.nt == 0) break;
+      const int sub = s ^ (c.items & 1);
+      if (!c.pair && sub >= c.nt) continue;  // a single tile: the other stream's
+      const int tile = c.tile0 + (c.pair ? sub : 0);
+      // this thread's row
+      int r;
+      bool valid;
+      int stride;
+      if (c.prefix) {
+        stride = p.pre_nb * p.pre_rb;
+        if (p.GT >= 128) {
+          r = tile % ((p.GT + 127) / 128) * 128 + x;
+          valid = r < p.GT;
+        } else {
+          const int i = x / p.GT;
+          r = x - i * p.GT;
+          valid = i < p.pre_nb && tile * p.pre_nb + i < p.n;
+        }
+      } else {
+        stride = p.own_rb;
+        r = tile * 128 + x;
+        valid = x < p.own_rb && r < p.GT;
+      }
+      const int vis = c.prefix ? c.len : c.len - (p.T - 1 - r % p.T);  // keys this row sees
+      const int vis_min = c.prefix ? c.len : c.len - (p.T - 1);
+      const bool any_valid = __any_sync(0xffffffffu, valid);
+      float m = -INFINITY, l = 0.f;
+      const int step = c.pair ? 1 : 2;
+      for (int j = c.pair ? 0 : sub; j < c.nt; j += step) {
+        const int key0 = 128 * (c.j0 + j);
+        if (!(ok = wait(&s_full[s], ns & 1))) break;
+        ++ns;
+        if (any_valid) {
+          tc_fence_after();
+          float sv[128];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32(s_addr + 32 * i, *reinterpret_cast<float(*)[32]>(&sv[32 * i]));
+          tc_wait_ld();
+          if (key0 + 128 > vis_min) {
+            const int lim = vis - key0;
+#pragma unroll
+            for (int i = 0; i < 128; ++i) sv[i] = i < lim ? sv[i] : -INFINITY;
+          }
+          float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+          for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], sv[i]);
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+          if (j < step) {
+            m = top;  // the piece's first tile on this stream: O starts from zero
+          } else if (__any_sync(0xffffffffu, top > m + kRescale)) {
+            // move the reference: S of this tile is ready, so the PV product
+            // before it (same issuing thread) is done and O is still
+            const float mn = fmaxf(m, top);
+            const float f = mn == -INFINITY ? 1.f : ex2_approx(m - mn);
+            l *= f;
+            m = mn;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+              float ov[32];
+              tmem_ld32(o_addr + 32 * i, ov);
+              tc_wait_ld();
+              uint32_t ou[32];
+#pragma unroll
+              for (int k = 0; k < 32; ++k) ou[k] = __float_as_uint(ov[k] * f);
+              tmem_st32(o_addr + 32 * i, ou);
+            }
+          }
+          const float neg = m == -INFINITY ? 0.f : -m;
+          float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const int k = 64 * h + 2 * i;
+              float x0, x1, x2, x3;
+              ffma2(x0, x1, sv[k], sv[k + 1], p.scale_log2, p.scale_log2, neg, neg);
+              ffma2(x2, x3, sv[k + 2], sv[k + 3], p.scale_log2, p.scale_log2, neg, neg);
+              x0 = ex2_approx(x0);
+              x1 = ex2_approx(x1);
+              x2 = ex2_approx(x2);
+              x3 = ex2_approx(x3);
+              fadd2(l0, l1, l0, l1, x0, x1);
+              fadd2(l2, l3, l2, l3, x2, x3);
+              pk[i] = pack_16x2<FP16>(x0, x1);
+              pk[i + 1] = pack_16x2<FP16>(x2, x3);
+            }
+            tmem_st32(s_addr + 32 * h, pk);
+          }
+          l += (l0 + l1) + (l2 + l3);
+          tc_wait_st();
+          tc_fence_before();
+        }
+        if (c.len - key0 < 128) {
+          // the segment's last tile: clear the V rows past its length
+          const int t = c.tiles + j, st = t % kSt;
+          if (!(ok = wait(&v_full[st], (t / kSt) & 1))) break;
+          const int first = c.len - key0, bytes = (128 - first) * 128;
+#pragma unroll
+          for (int ch = 0; ch < C::kChunks; ++ch) {
+            const uint32_t base = smem_u32(sV + st * C::kTile + ch * 16384) + first * 128;
+            for (int o = x * 16; o < bytes; o += 128 * 16) st_shared_v4(base + o, 0u, 0u, 0u, 0u);
+          }
+          fence_async_shared();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[s]);
+      }
+      if (!ok) break;
+      // the piece's part
+      if (!(ok = wait(&o_full[s], no & 1))) break;
+      ++no;
+      if (any_valid) {
+        tc_fence_after();
+        const long long at =
+            (c.prefix ? 0 : p.pre_slots) + (static_cast<long long>(c.slot) * 2 + sub) * stride + x;
+        float* po = p.part_o + at * D;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          float ov[32];
+          tmem_ld32(o_addr + 32 * i, ov);
+          tc_wait_ld();
+          if (valid) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<float4*>(po + 32 * i + k) = make_float4(ov[k], ov[k + 1], ov[k + 2], ov[k + 3]);
+          }
+        }
+        if (valid) p.part_ml[at] = make_float2(m, l);
+        tc_fence_before();
+      }
+      __syncwarp();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// ------------------------------------------------------------------ merge
+// One output row per block: with M the largest reference of its parts,
+//   out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p.
+// The parts of a row are found from the schedule alone (segment offsets and
+// grid size); warps take them in turn, and the order of the sums is fixed.
+constexpr int kMergeThreads = 128;
+
+template <int D, bool FP16>
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p, int grid, uint16_t* out, float* lse) {
+  constexpr int kV = D / 32;  // values per lane
+  __shared__ float so[4][D];
+  __shared__ float2 sml[4];
+  grid_dep_launch();
+  grid_dep_wait();
+  const int row = blockIdx.x;  // (b, hkv, r)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bh = row / p.GT, r = row - bh * p.GT;
+  const int b = bh / p.Hkv, hkv = bh - b * p.Hkv;
+  const long long W = p.seg_off[p.nseg];
+  float acc[kV];
+#pragma unroll
+  for (int i = 0; i < kV; ++i) acc[i] = 0.f;
+  float m = -INFINITY, l = 0.f;
+  int turn = 0;
+  for (int half = 0; half < 2; ++half) {
+    // half 0: the prefix, 1: the cache
+    if (half == 0 ? p.npre == 0 : p.nseg == p.npre) continue;
+    const int seg = half == 0 ? b / p.n : p.npre + b;
+    const long long off = p.seg_off[seg];
+    const int up = half == 0 ? p.pre_up : p.own_up, rt = half == 0 ? p.pre_rt : p.own_rt;
+    const int nkt = static_cast<int>((p.seg_off[seg + 1] - off) / (p.Hkv * up));
+    if (nkt == 0) continue;
+    int tile, x, stride;
+    if (half == 0) {
+      const int i = b - seg * p.n;
+      stride = p.pre_nb * p.pre_rb;
+      if (p.GT >= 128) {
+        tile = i * ((p.GT + 127) / 128) + r / 128;
+        x = r % 128;
+      } else {
+        tile = i / p.pre_nb;
+        x = (i - tile * p.pre_nb) * p.GT + r;
+      }
+    } else {
+      stride = p.own_rb;
+      tile = r / 128;
+      x = r % 128;
+    }
+    const int lu = hkv * up + (tile >> 1);
+    const bool pair = (tile | 1) < rt;
+    const long long o0 = off + static_cast<long long>(lu) * nkt, o1 = o0 + nkt;
+    const int c0 = static_cast<int>(((o0 + 1) * grid - 1) / W), c1 = static_cast<int>((o1 * grid - 1) / W);
+    const long long unit = static_cast<long long>(half == 0 ? seg : b) * p.Hkv * up + lu;
+    const long long base = half == 0 ? 0 : p.pre_slots;
+    const int nsub = pair ? 1 : 2;
+    for (int q = (warp - turn) & 3; q < (c1 - c0 + 1) * nsub; q += 4) {
+      const int c = c0 + (pair ? q : q >> 1);
+      const int sub = pair ? (tile & 1) : (q & 1);
+      const long long lo = max(o0, W * c / grid), hi = min(o1, W * (c + 1) / grid);
+      if (hi <= lo || (!pair && sub >= hi - lo)) continue;
+      const long long at = base + ((unit + c) * 2 + sub) * stride + x;
+      const float2 ml = p.part_ml[at];
+      float v[kV];
+      const float* src = p.part_o + at * D + lane * kV;
+      if constexpr (kV == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(src);
+        v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+      } else {
+        const float2 f = *reinterpret_cast<const float2*>(src);
+        v[0] = f.x, v[1] = f.y;
+      }
+      if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing visible in this part
+      const float mn = fmaxf(m, ml.x);
+      const float fa = m == -INFINITY ? 0.f : ex2_approx(m - mn);
+      const float fb = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mn);
+      m = mn;
+      l = l * fa + ml.y * fb;
+#pragma unroll
+      for (int i = 0; i < kV; ++i) acc[i] = acc[i] * fa + v[i] * fb;
+    }
+    turn += (c1 - c0 + 1) * nsub;
+  }
+  if (lane == 0) sml[warp] = make_float2(m, l);
+#pragma unroll
+  for (int i = 0; i < kV; ++i) so[warp][lane * kV + i] = acc[i];
+  __syncthreads();
+  float M = -INFINITY, L = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) M = fmaxf(M, sml[w].x);
+  float f[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    f[w] = sml[w].x == -INFINITY && sml[w].y == 0.f ? 0.f : ex2_approx(sml[w].x - M);
+    L += f[w] * sml[w].y;
+  }
+  const bool empty = M == -INFINITY && L == 0.f;
+  for (int i = 2 * threadIdx.x; i < D; i += 2 * kMergeThreads) {
+    float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      a0 += f[w] * so[w][i];
+      a1 += f[w] * so[w][i + 1];
+    }
+    const uint32_t u = empty ? 0u : pack_16x2<FP16>(a0 / L, a1 / L);
+    *reinterpret_cast<uint32_t*>(out + static_cast<long long>(row) * D + i) = u;
+  }
+  if (lse && threadIdx.x == 0) lse[row] = empty ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
+
+struct Plan {
+  Params p = {};
+  long long pre_units = 0, own_units = 0, part_rows = 0;
+  size_t off_seg = 0, off_ml = 0, off_o = 0, total = 0;
+};
+
+// Everything that follows from the sizes alone.
+bool make_plan(Plan& w, int B, int G, int Hkv, int T, int d, int Bp, int P, int C) {
+  Params& p = w.p;
+  p.B = B;
+  p.G = G;
+  p.Hkv = Hkv;
+  p.T = T;
+  p.Bp = Bp;
+  p.n = B / Bp;
+  p.P = P;
+  p.C = C;
+  p.GT = G * T;
+  p.npre = P > 0 ? Bp : 0;
+  p.nseg = p.npre + (C > 0 ? B : 0);
+  if (p.GT >= 128) {
+    p.pre_nb = 1;
+    p.pre_rb = 128;
+    p.pre_rt = p.n * ((p.GT + 127) / 128);
+  } else {
+    p.pre_nb = 128 / p.GT < p.n ? 128 / p.GT : p.n;
+    p.pre_rb = p.GT;
+    p.pre_rt = (p.n + p.pre_nb - 1) / p.pre_nb;
+  }
+  p.pre_up = (p.pre_rt + 1) / 2;
+  p.own_rb = p.GT < 128 ? p.GT : 128;
+  p.own_rt = (p.GT + 127) / 128;
+  p.own_up = (p.own_rt + 1) / 2;
+  w.pre_units = P > 0 ? static_cast<long long>(Bp) * Hkv * p.pre_up : 0;
+  w.own_units = C > 0 ? static_cast<long long>(B) * Hkv * p.own_up : 0;
+  const long long tiles = w.pre_units * ((P + 127LL) / 128) + w.own_units * ((C + 127LL) / 128);
+  if (w.pre_units + w.own_units > (1LL << 30) || tiles > (1LL << 50)) return false;
+  p.pre_slots = P > 0 ? (w.pre_units + kMaxCtas) * 2 * p.pre_nb * p.pre_rb : 0;
+  w.part_rows = p.pre_slots + (C > 0 ? (w.own_units + kMaxCtas) * 2 * p.own_rb : 0);
+  size_t o = 256;
+  w.off_seg = o;
+  o += align256(static_cast<size_t>(p.nseg + 1) * 8);
+  w.off_ml = o;
+  o += align256(static_cast<size_t>(w.part_rows) * 8);
+  w.off_o = o;
+  o += align256(static_cast<size_t>(w.part_rows) * d * 4);
+  w.total = o;
+  return true;
+}
+
+template <int D, bool FP16>
+cudaError_t run(const DecodeLaunch& a, const Plan& w, const CUtensorMap (&m)[6], int grid, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             Cfg<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  const cudaError_t e2 = launch_chained(decode_kernel<D, FP16>, dim3(grid), dim3(kThreads), Cfg<D>::kSmem, st, m[0],
+                                        m[1], m[2], m[3], m[4], m[5], w.p);
+  if (e2 != cudaSuccess) return e2;
+  return launch_chained(merge_kernel<D, FP16>, dim3(static_cast<unsigned>(a.B) * a.Hkv * w.p.GT), dim3(kMergeThreads),
+                        0, st, w.p, grid, static_cast<uint16_t*>(a.out), a.lse);
+}
+
+}  // namespace
+
+size_t decode_workspace_bytes(int B, int G, int Hkv, int T, int d, int Bp, int P, int C) {
+  Plan w;
+  return make_plan(w, B, G, Hkv, T, d, Bp, P, C) ? w.total : 0;
+}
+
+cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t st) {
+  Plan w;
+  if (!make_plan(w, a.B, a.G, a.Hkv, a.T, a.d, a.Bp, a.P, a.C)) return cudaErrorInvalidValue;
+  Params& p = w.p;
+  p.prefix_len = a.prefix_len;
+  p.cache_len = a.cache_len;
+  p.scale_log2 = 1.4426950408889634f / (a.d == 128 ? 11.313708498984761f : 8.0f);
+  p.status = reinterpret_cast<int*>(a.ws);
+  p.seg_off = reinterpret_cast<long long*>(a.ws + w.off_seg);
+  p.part_ml = reinterpret_cast<float2*>(a.ws + w.off_ml);
+  p.part_o = reinterpret_cast<float*>(a.ws + w.off_o);
+  // Q: [B][Hkv][G T][d]; prefix tiles take pre_nb sequences at once
+  CUtensorMap m[6];
+  const uint64_t u = 1;
+  const uint64_t dq[4] = {u * a.d, u * p.GT, u * a.Hkv, u * a.B};
+  const uint32_t bp[4] = {64, static_cast<uint32_t>(p.pre_rb), 1, static_cast<uint32_t>(p.pre_nb)};
+  const uint32_t bc[4] = {64, static_cast<uint32_t>(p.own_rb), 1, 1};
+  const uint32_t bk[3] = {64, 64, 1};
+  const uint64_t dp[3] = {u * a.d, u * a.P, u * a.Bp * a.Hkv}, dc[3] = {u * a.d, u * a.C, u * a.B * a.Hkv};
+  CUresult r = encode_tensor_map_16(&m[0], a.q, a.fp16, 4, dq, bp);
+  if (r == CUDA_SUCCESS) r = encode_tensor_map_16(&m[1], a.q, a.fp16, 4, dq, bc);
+  if (a.P > 0) {
+    if (r == CUDA_SUCCESS) r = encode_tensor_map_16(&m[2], a.k_prefix, a.fp16, 3, dp, bk);
+    if (r == CUDA_SUCCESS) r = encode_tensor_map_16(&m[3], a.v_prefix, a.fp16, 3, dp, bk);
+  }
+  if (a.C > 0) {
+    if (r == CUDA_SUCCESS) r = encode_tensor_map_16(&m[4], a.k_cache, a.fp16, 3, dc, bk);
+    if (r == CUDA_SUCCESS) r = encode_tensor_map_16(&m[5], a.v_cache, a.fp16, 3, dc, bk);
+  }
+  if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+  if (a.P == 0) m[2] = m[4], m[3] = m[5];
+  if (a.C == 0) m[4] = m[2], m[5] = m[3];
+  // one CTA per SM; no more than there can be tiles
+  const long long tiles = w.pre_units * ((a.P + 127LL) / 128) + w.own_units * ((a.C + 127LL) / 128);
+  int grid = device_sm_count();
+  if (grid > kMaxCtas) grid = kMaxCtas;
+  if (tiles < grid) grid = static_cast<int>(tiles < 1 ? 1 : tiles);
+  if (a.d == 128)
+    return a.fp16 ? run<128, true>(a, w, m, grid, st) : run<128, false>(a, w, m, grid, st);
+  return a.fp16 ? run<64, true>(a, w, m, grid, st) : run<64, false>(a, w, m, grid, st);
+}
+
+}  // namespace psa

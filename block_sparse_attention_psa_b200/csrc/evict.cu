@@ -1,0 +1,422 @@
+// evict.cu -- eviction from a key/value cache by accumulated attention
+// weight: which entries stay (select_kernel) and the move of their rows
+// (move_kernel).
+//
+// For one (sequence, KV head) with len entries and nk = min(len, budget):
+// every entry gets a 32-bit key that orders as its score does (protected
+// entries above all), the nk-th largest key K* is found by a radix select of
+// 11 + 11 + 10 bits, and an entry stays iff key > K*, or key == K* and it is
+// among the first (nk - #{key > K*}) such entries in slot order.  Slots below
+// nk whose entry stays keep it; the r-th hole (ascending) takes the r-th
+// survivor from slot nk on (ascending).  Sources lie at or past nk and
+// destinations below it, so the move is free of hazards in place, and a step
+// that evicts one entry moves one row.
+//
+// select_kernel is bound by its passes over the slots of one head and by the
+// block-wide steps between them, so a head is split over a cluster of up to 8
+// CTAs: each keeps its slice's keys in shared memory and histograms, counts
+// and ranks are combined through distributed shared memory.  Scores and
+// positions are read from DRAM once.  Every warp owns a contiguous run of
+// slots, so ranks in slot order need one scan over warps and one over CTAs,
+// and no barrier inside the runs.
+// move_kernel is a gather of 2d-byte rows: 16 bytes per lane, K and V rows of
+// several slots in flight per warp; bound by DRAM.
+#include <climits>
+#include <cooperative_groups.h>
+
+#include "internal.h"
+#include "sm100.cuh"
+
+namespace psa {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kBins = 2048;
+constexpr int kSmemKeys = 32768;  // keys of a slice kept on chip (128 KB); a longer slice is read again per pass
+constexpr int kMaxThreads = 1024;
+
+struct SelectParams {
+  const float* score;
+  const int* pos;        // null: the slot index
+  const int* cache_len;  // null: C
+  int* kept;             // [B * Hkv][budget]
+  int* late;             // scratch [B * Hkv][budget]: survivors from slot nk on, ascending
+  int* nk_out;           // scratch [B]
+  int* status;
+  int B, Hkv, C, budget, sink, recent;
+  int slice;             // slots per CTA, a multiple of 32 * warps
+  int keys_on_chip;
+};
+
+// Order-preserving key of a score: NaN as the lowest (-inf), -0 as +0.
+__device__ __forceinline__ uint32_t score_key(float f) {
+  if (f != f) f = -INFINITY;
+  const uint32_t b = __float_as_uint(f + 0.0f);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+// Exclusive prefix over the cluster's CTAs of one int per CTA, and the total.
+// `box` is written and read by this call alone.
+__device__ __forceinline__ int cluster_exclusive(cg::cluster_group& cl, int* box, int mine, int& total) {
+  if (threadIdx.x == 0) *box = mine;
+  cl.sync();
+  int before = 0;
+  total = 0;
+  for (unsigned r = 0; r < cl.num_blocks(); ++r) {
+    const int v = *cl.map_shared_rank(box, r);
+    if (r < cl.block_rank()) before += v;
+    total += v;
+  }
+  return before;
+}
+
+// Exclusive prefix over the block's warps of a warp-uniform value, and the
+// block's total.  `buf` holds 33 ints.
+__device__ __forceinline__ int warps_exclusive(int* buf, int mine, int& total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  __syncthreads();
+  if (lane == 0) buf[warp] = mine;
+  __syncthreads();
+  if (warp == 0) {
+    const int v = lane < warps ? buf[lane] : 0;
+    int s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += u;
+    }
+    __syncwarp();
+    buf[lane] = s - v;
+    if (lane == 31) buf[32] = s;
+  }
+  __syncthreads();
+  total = buf[32];
+  return buf[warp];
+}
+
+__global__ void __launch_bounds__(kMaxThreads, 1) select_kernel(const SelectParams p) {
+  extern __shared__ uint32_t smem[];
+  __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t sum[kBins];
+  __shared__ int buf[33];
+  __shared__ int box[4];
+  __shared__ uint32_t pick[2];  // chosen bin, keys above it
+  cg::cluster_group cl = cg::this_cluster();
+  const int rank = static_cast<int>(cl.block_rank());
+  const int ncta = static_cast<int>(cl.num_blocks());
+  const int bh = blockIdx.x / ncta;
+  const int b = bh / p.Hkv;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x;
+  uint32_t* stay = smem;                      // one bit per slot of the slice
+  uint32_t* keys = smem + (p.slice >> 5);     // the slice's keys (when they fit)
+  grid_dep_launch();
+  grid_dep_wait();
+
+  int len = p.cache_len ? __ldg(p.cache_len + b) : p.C;
+  len = min(max(len, 0), p.C);
+  if (blockIdx.x == 0) {
+    // one writer of the status word: the lengths of all sequences
+    bool bad = false;
+    if (p.cache_len)
+      for (int i = tid; i < p.B; i += nthr) {
+        const int n = __ldg(p.cache_len + i);
+        bad |= n < 0 || n > p.C;
+      }
+    bad = __syncthreads_or(bad);
+    if (tid == 0) *p.status = bad ? kStatusLength : 0;
+  }
+  const int nk = min(len, p.budget);
+  if (rank == 0 && bh % p.Hkv == 0 && tid == 0) p.nk_out[b] = nk;
+  int* kept = p.kept + static_cast<long long>(bh) * p.budget;
+  int* late = p.late + static_cast<long long>(bh) * p.budget;
+  const float* score = p.score + static_cast<long long>(bh) * p.C;
+  const int* pos = p.pos ? p.pos + static_cast<long long>(bh) * p.C : nullptr;
+
+  for (int i = nk + rank * nthr + tid; i < p.budget; i += ncta * nthr) kept[i] = -1;
+  if (len <= p.budget) {  // the same for the whole cluster
+    for (int i = rank * nthr + tid; i < nk; i += ncta * nthr) kept[i] = i;
+    return;
+  }
+
+  // ---- the latest position of the head
+  const int s0 = rank * p.slice, s1 = min(s0 + p.slice, len);
+  int last = len - 1;
+  if (pos) {
+    last = INT_MIN;
+    for (int i = s0 + tid; i < s1; i += nthr) last = max(last, __ldg(pos + i));
+    last = __reduce_max_sync(0xffffffffu, last);
+    if (lane == 0) buf[warp] = last;
+    __syncthreads();
+    if (tid == 0) {
+      for (int w = 1; w < (nthr >> 5); ++w) last = max(last, buf[w]);
+      box[0] = last;
+    }
+    cl.sync();
+    for (int r = 0; r < ncta; ++r) last = max(last, *cl.map_shared_rank(&box[0], r));
+    last = __shfl_sync(0xffffffffu, last, 0);
+  }
+  // positions after `last - recent` are protected; 64 bits, so that no
+  // position a caller stores can wrap it
+  const long long guard = static_cast<long long>(last) - p.recent;
+  auto make_key = [&](int i) -> uint32_t {
+    const int at = pos ? __ldg(pos + i) : i;
+    if (at < p.sink || at > guard) return 0xffffffffu;
+    return score_key(__ldg(score + i));
+  };
+  if (p.keys_on_chip)
+    for (int i = s0 + tid; i < s1; i += nthr) keys[i - s0] = make_key(i);
+  auto key = [&](int i) -> uint32_t { return p.keys_on_chip ? keys[i - s0] : make_key(i); };
+  __syncthreads();
+
+  // ---- radix select of the nk-th largest key
+  uint32_t prefix = 0, need = static_cast<uint32_t>(nk);
+#pragma unroll
+  for (int round = 0; round < 3; ++round) {
+    const int shift = round == 0 ? 21 : (round == 1 ? 10 : 0);
+    const int bits = round == 2 ? 10 : 11;
+    const int above = shift + bits;  // bits already decided start here
+    const uint32_t mask = (1u << bits) - 1u;
+    for (int i = tid; i < kBins; i += nthr) hist[i] = 0u;
+    __syncthreads();
+    const int trips = (s1 - s0 + nthr - 1) / nthr;
+    for (int it = 0; it < trips; ++it) {
+      const int i = s0 + it * nthr + tid;
+      uint32_t bin = 0xffffffffu;
+      if (i < s1) {
+        const uint32_t k = key(i);
+        if (round == 0 || (k >> above) == prefix) bin = (k >> shift) & mask;
+      }
+      // a warp whose keys share one bin (equal scores) adds once
+      int same;
+      __match_all_sync(0xffffffffu, bin, &same);
+      if (same) {
+        if (lane == 0 && bin != 0xffffffffu) atomicAdd(&hist[bin], 32u);
+      } else if (bin != 0xffffffffu) {
+        atomicAdd(&hist[bin], 1u);
+      }
+    }
+    cl.sync();
+    for (int i = tid; i < kBins; i += nthr) {
+      uint32_t s = 0;
+      for (int r = 0; r < ncta; ++r) s += *cl.map_shared_rank(&hist[i], r);
+      sum[i] = s;
+    }
+    cl.sync();  // the remote histograms may be cleared again (and sum[] is complete)
+    // bins from the top: the first warp scans 64 per lane
+    if (warp == 0) {
+      constexpr int kPer = kBins / 32;
+      uint32_t s = 0;
+      for (int j = 0; j < kPer; ++j) s += sum[kBins - 1 - (lane * kPer + ((j + lane) % kPer))];
+      uint32_t inc = s;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+      }
+      uint32_t at = inc - s;  // keys in the bins above this lane's
+      if (at < need && need <= inc) {
+        for (int j = 0; j < kPer; ++j) {
+          const int bin = kBins - 1 - (lane * kPer + j);
+          if (at + sum[bin] >= need) {
+            pick[0] = static_cast<uint32_t>(bin);
+            pick[1] = at;
+            break;
+          }
+          at += sum[bin];
+        }
+      }
+    }
+    __syncthreads();
+    prefix = (prefix << bits) | pick[0];
+    need -= pick[1];
+    __syncthreads();
+  }
+  // prefix is K*; `need` entries with that key stay
+
+  // ---- which entries stay; each warp owns the slots [w0, w1)
+  const int per_warp = p.slice / (nthr >> 5);
+  const int w0 = min(s0 + warp * per_warp, s1), w1 = min(w0 + per_warp, s1);
+  int eq = 0;
+  for (int i = w0 + lane; i - lane < w1; i += 32)
+    eq += __popc(__ballot_sync(0xffffffffu, i < w1 && key(i) == prefix));
+  int total, all;
+  int eq_at = warps_exclusive(buf, eq, total);
+  eq_at += cluster_exclusive(cl, &box[1], total, all);
+  int holes = 0, lates = 0;
+  for (int i = w0 + lane; i - lane < w1; i += 32) {
+    const uint32_t k = i < w1 ? key(i) : 0u;
+    const uint32_t tie = __ballot_sync(0xffffffffu, i < w1 && k == prefix);
+    const int before = eq_at + __popc(tie & ((1u << lane) - 1u));
+    const bool in = i < w1 && (k > prefix || (k == prefix && before < static_cast<int>(need)));
+    eq_at += __popc(tie);
+    const uint32_t word = __ballot_sync(0xffffffffu, in);
+    if (lane == 0) stay[(i - s0) >> 5] = word;
+    holes += __popc(__ballot_sync(0xffffffffu, i < w1 && i < nk && !in));
+    lates += __popc(__ballot_sync(0xffffffffu, in && i >= nk));
+  }
+  int hole_at = warps_exclusive(buf, holes, total);
+  hole_at += cluster_exclusive(cl, &box[2], total, all);
+  int late_at = warps_exclusive(buf, lates, total);
+  late_at += cluster_exclusive(cl, &box[3], total, all);
+  __syncwarp();
+  for (int i = w0 + lane; i - lane < w1; i += 32) {
+    const uint32_t word = stay[(i - s0) >> 5];
+    const bool in = (word >> lane) & 1u;
+    const uint32_t far = __ballot_sync(0xffffffffu, in && i >= nk);
+    if (in && i >= nk) late[late_at + __popc(far & ((1u << lane) - 1u))] = i;
+    late_at += __popc(far);
+  }
+  cl.sync();  // orders the list's global writes for the cluster
+  for (int i = w0 + lane; i - lane < w1; i += 32) {
+    const uint32_t word = stay[(i - s0) >> 5];
+    const bool in = (word >> lane) & 1u;
+    const bool hole = i < w1 && i < nk && !in;
+    const uint32_t open = __ballot_sync(0xffffffffu, hole);
+    if (hole) kept[i] = *(volatile int*)(late + hole_at + __popc(open & ((1u << lane) - 1u)));
+    if (in && i < nk) kept[i] = i;
+    hole_at += __popc(open);
+  }
+  cl.sync();  // no CTA leaves while another may read its shared memory
+}
+
+struct MoveParams {
+  const uint4* k;
+  const uint4* v;
+  const float* score;
+  const int* pos;
+  const int* kept;
+  const int* nk;
+  uint4* k_out;
+  uint4* v_out;
+  float* score_out;
+  int* pos_out;
+  int* len_out;
+  int B, Hkv, C, C_out, budget;
+  int in_place, chunks;
+};
+
+constexpr int kMoveThreads = 256;
+constexpr int kMoveSlots = 64;  // slots per CTA: 8 per warp, K and V rows 16 bytes per lane
+
+template <int D>
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) {
+  constexpr int kLanes = D / 8;           // 16-byte pieces of a row
+  constexpr int kRows = 32 / kLanes;      // rows per warp-wide access
+  constexpr int kPerWarp = kMoveSlots / (kMoveThreads / 32);
+  constexpr int kSteps = kPerWarp / kRows;
+  grid_dep_launch();
+  grid_dep_wait();
+  const int bh = blockIdx.x / p.chunks, chunk = blockIdx.x - bh * p.chunks;
+  const int slot0 = chunk * kMoveSlots;
+  const int* kept = p.kept + static_cast<long long>(bh) * p.budget;
+  const long long in0 = static_cast<long long>(bh) * p.C, out0 = static_cast<long long>(bh) * p.C_out;
+  if (chunk == 0 && bh % p.Hkv == 0 && threadIdx.x == 0) p.len_out[bh / p.Hkv] = p.nk[bh / p.Hkv];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = lane / kLanes, piece = lane % kLanes;
+  int src[kSteps];
+  uint4 kr[kSteps], vr[kSteps];
+#pragma unroll
+  for (int j = 0; j < kSteps; ++j) {
+    const int i = slot0 + warp * kPerWarp + j * kRows + sub;
+    src[j] = i < p.budget ? __ldg(kept + i) : -1;
+    if (p.in_place && src[j] == i) src[j] = -1;
+  }
+#pragma unroll
+  for (int j = 0; j < kSteps; ++j)
+    if (src[j] >= 0) {
+      kr[j] = p.k[(in0 + src[j]) * kLanes + piece];
+      vr[j] = p.v[(in0 + src[j]) * kLanes + piece];
+    }
+#pragma unroll
+  for (int j = 0; j < kSteps; ++j)
+    if (src[j] >= 0) {
+      const long long o = (out0 + slot0 + warp * kPerWarp + j * kRows + sub) * kLanes + piece;
+      p.k_out[o] = kr[j];
+      p.v_out[o] = vr[j];
+    }
+  if (threadIdx.x < kMoveSlots) {
+    const int i = slot0 + threadIdx.x;
+    const int s = i < p.budget ? __ldg(kept + i) : -1;
+    if (s >= 0) {
+      // in place a slot that stays still needs its position when none came in
+      if (!(p.in_place && s == i)) p.score_out[out0 + i] = p.score[in0 + s];
+      if (!(p.in_place && p.pos && s == i)) p.pos_out[out0 + i] = p.pos ? p.pos[in0 + s] : s;
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const EvictLaunch& a, cudaStream_t st) {
+  SelectParams s = {};
+  s.score = a.score;
+  s.pos = a.pos;
+  s.cache_len = a.cache_len;
+  s.kept = a.kept;
+  s.late = a.late;
+  s.nk_out = a.nk;
+  s.status = a.status;
+  s.B = a.B;
+  s.Hkv = a.Hkv;
+  s.C = a.C;
+  s.budget = a.budget;
+  s.sink = a.sink;
+  s.recent = a.recent;
+  // CTAs per head: slices of about 4096 slots, while the heads alone do not
+  // fill the machine (a cluster costs its barriers); 8 is the portable limit
+  const long long heads = static_cast<long long>(a.B) * a.Hkv;
+  int ncta = 1;
+  while (ncta < 8 && a.C > 4096 * ncta && heads * ncta * 2 <= 296) ncta *= 2;
+  while (ncta < 8 && (a.C + ncta - 1) / ncta > kSmemKeys) ncta *= 2;
+  const int part = (a.C + ncta - 1) / ncta;
+  int threads = kMaxThreads;
+  while (threads > 128 && threads * 4 > part) threads /= 2;
+  s.slice = (part + threads - 1) / threads * threads;
+  s.keys_on_chip = s.slice <= kSmemKeys;
+  const size_t smem = static_cast<size_t>(s.slice / 32 + (s.keys_on_chip ? s.slice : 0)) * 4;
+  cudaError_t e = cudaSuccess;
+  if (smem > 24 * 1024)
+    e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 180 * 1024);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(heads * ncta));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(ncta);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if ((e = cudaLaunchKernelEx(&cfg, select_kernel, s)) != cudaSuccess) return e;
+
+  MoveParams m = {};
+  m.k = reinterpret_cast<const uint4*>(a.k);
+  m.v = reinterpret_cast<const uint4*>(a.v);
+  m.score = a.score;
+  m.pos = a.pos;
+  m.kept = a.kept;
+  m.nk = a.nk;
+  m.k_out = reinterpret_cast<uint4*>(a.k_out);
+  m.v_out = reinterpret_cast<uint4*>(a.v_out);
+  m.score_out = a.score_out;
+  m.pos_out = a.pos_out;
+  m.len_out = a.len_out;
+  m.B = a.B;
+  m.Hkv = a.Hkv;
+  m.C = a.C;
+  m.C_out = a.C_out;
+  m.budget = a.budget;
+  m.in_place = a.k == a.k_out;
+  m.chunks = (a.budget + kMoveSlots - 1) / kMoveSlots;
+  const dim3 grid(static_cast<unsigned>(heads * m.chunks));
+  return a.d == 128 ? launch_chained(move_kernel<128>, grid, dim3(kMoveThreads), 0, st, m)
+                    : launch_chained(move_kernel<64>, grid, dim3(kMoveThreads), 0, st, m);
+}
+
+}  // namespace psa

@@ -166,12 +166,54 @@ cudaError_t launch_hyd_stat(const uint16_t* k, const uint16_t* v, const float* k
 cudaError_t launch_hyd_apply(const uint16_t* q, const float* hstat, const float* w, uint16_t* out, int BH, int N,
                              int d, int* status, cudaStream_t st);
 
+// decode.cu: attention of new tokens over a shared prefix and their own caches
+struct DecodeLaunch {
+  const void* q;        // [B, Hkv * G, T, d]
+  const void* k_prefix; // [Bp, Hkv, P, d] (null when P == 0)
+  const void* v_prefix;
+  const int* prefix_len;  // [Bp], null: P
+  const void* k_cache;  // [B, Hkv, C, d] (null when C == 0)
+  const void* v_cache;
+  const int* cache_len;   // [B], null: C
+  int B, G, Hkv, T, d, Bp, P, C;
+  bool fp16;
+  void* out;
+  float* lse;           // nullable
+  char* ws;
+};
+// bytes of workspace, 0 if the sizes overflow what the schedule can count
+size_t decode_workspace_bytes(int B, int G, int Hkv, int T, int d, int Bp, int P, int C);
+cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t st);
+
+// evict.cu: eviction from a cache by accumulated weight
+struct EvictLaunch {
+  const void* k;        // 16-bit [B, Hkv, C, d]
+  const void* v;
+  const float* score;   // [B, Hkv, C]
+  const int* pos;       // [B, Hkv, C], null: the slot index
+  const int* cache_len; // [B], null: C
+  int B, Hkv, C, d, budget, sink, recent, C_out;
+  void* k_out;          // 16-bit [B, Hkv, C_out, d]
+  void* v_out;
+  float* score_out;
+  int* pos_out;
+  int* len_out;         // [B]
+  int* kept;            // [B, Hkv, budget]
+  int* status;          // workspace: status word,
+  int* nk;              // [B],
+  int* late;            // [B, Hkv, budget]
+};
+cudaError_t launch_evict(const EvictLaunch& a, cudaStream_t st);
+
 // api.cu: one-shot flag set by psa_test_stall_next_attn, taken by the next psa_attn
 int take_stall_request();
 
 // api.cu: driver entry point for cuTensorMapEncodeTiled (resolved once)
 CUresult encode_tensor_map_3d_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows,
                                    uint64_t outer, uint32_t box_inner, uint32_t box_rows);
+// 16-bit tensor of rank 3 or 4, dims innermost first and dense; 128-byte swizzle
+CUresult encode_tensor_map_16(CUtensorMap* map, const void* base, bool fp16, int rank, const uint64_t* dims,
+                              const uint32_t* box);
 int device_sm_count();
 // PSA_OK if the current device is sm_100 and every non-null pointer names
 // device (or managed) memory of that device; else PSA_ERR_DEVICE / PSA_ERR_ARG.

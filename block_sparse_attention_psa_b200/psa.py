@@ -28,11 +28,16 @@ PSA_ERR_CUDA = 5
 PSA_ERR_TIMEOUT = 6
 PSA_ERR_CSR = 7
 PSA_ERR_DEVICE = 8
+PSA_ERR_LENGTH = 9
+
+PSA_BF16 = 0
+PSA_FP16 = 1
 
 EXPORTS = ("psa_status_string", "psa_version", "psa_workspace_size", "psa_route_capacity", "psa_pool",
            "psa_route_topk", "psa_route_thresh", "psa_attn", "psa_dense", "psa_read_status",
            "psa_attn_noalloc", "psa_route_thresh_prob", "psa_test_stall_next_attn",
-           "psa_read_fixup_count", "psa_hyd_stat", "psa_attn_hyd", "psa_attn_bwd")
+           "psa_read_fixup_count", "psa_hyd_stat", "psa_attn_hyd", "psa_attn_bwd", "psa_decode_workspace_size",
+           "psa_decode", "psa_cache_evict_workspace_size", "psa_cache_evict")
 
 _lib = None
 
@@ -61,6 +66,10 @@ def _declare(L: ctypes.CDLL) -> None:
         "psa_hyd_stat": (I, [P, P, P, P, I, I, I, I, P, P, Z, P]),
         "psa_attn_bwd": (I, [P, P, P, P, P, P, P, Z, I, I, I, I, I, I, P, P, P, P, P, P, P, Z, P]),
         "psa_attn_hyd": (I, [P, P, P, P, P, P, P, P, Z, P, I, I, I, I, I, I, P, P, P, Z, P]),
+        "psa_decode_workspace_size": (Z, [I] * 8),
+        "psa_decode": (I, [P] * 7 + [I] * 9 + [P, P, P, Z, P]),
+        "psa_cache_evict_workspace_size": (Z, [I] * 4),
+        "psa_cache_evict": (I, [P] * 5 + [I] * 8 + [P] * 7 + [Z, P]),
         "psa_test_stall_next_attn": (I, [I]),
         "psa_attn_noalloc": (I, [P, P, P, P, P, P, P, Z, P, I, I, I, I, I, I, P, P, P, P]),
     }
@@ -395,6 +404,138 @@ def psa_attn_noalloc(q, k, v, kbar, vsum, row_ptr, col_idx, causal: bool = False
           _ptr(col_idx), col_idx.numel(), _ptr(row_max), B, H, N, d, block_size, int(causal), _ptr(out),
           _ptr(lse), _ptr(status), _stream(stream, q))
     return out
+
+
+_DTYPES = {torch.bfloat16: PSA_BF16, torch.float16: PSA_FP16}
+
+
+def _dtype16(name, t):
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def _shape4(name, t):
+    if t.dim() != 4:
+        raise ValueError(f"{name} must have 4 dimensions, got {tuple(t.shape)}")
+    return tuple(t.shape)
+
+
+def _serve_ws(fn, n, device):
+    if n == 0:
+        raise PSAError(fn, PSA_ERR_ARG)
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def psa_decode_workspace_size(B: int, Hq: int, Hkv: int, T: int, d: int, Bp: int = 1, P: int = 0, C: int = 0) -> int:
+    return int(lib().psa_decode_workspace_size(B, Hq, Hkv, T, d, Bp, P, C))
+
+
+def decode_workspace(B, Hq, Hkv, T, d, Bp=1, P=0, C=0, device=None) -> torch.Tensor:
+    """A device workspace of psa_decode_workspace_size bytes."""
+    return _serve_ws("psa_decode_workspace_size", psa_decode_workspace_size(B, Hq, Hkv, T, d, Bp, P, C), device)
+
+
+def psa_decode(q, k_cache=None, v_cache=None, cache_len=None, k_prefix=None, v_prefix=None, prefix_len=None,
+               ws=None, out=None, lse=None, want_lse: bool = False, stream=None):
+    """Attention of new tokens q [B, Hq, T, d] (bf16 or fp16) over a prefix
+    [Bp, Hkv, P, d] that groups of B / Bp sequences share and each sequence's
+    own cache [B, Hkv, C, d], in one softmax.  ``prefix_len`` [Bp] and
+    ``cache_len`` [B] (int32, None: the capacity) are the valid lengths; the
+    last T valid cache entries are the new tokens (query t sees slots below
+    cache_len - (T - 1 - t)).  Returns out and, if requested, lse (float32
+    [B, Hq, T])."""
+    B, Hq, T, d = _shape4("q", q)
+    dt = _dtype16("q", q)
+    if k_cache is None and k_prefix is None:
+        raise ValueError("a cache or a prefix is required")
+    Bp, P, C, Hkv = 1, 0, 0, 0
+    if k_prefix is not None:
+        Bp, Hkv, P, _ = _shape4("k_prefix", k_prefix)
+        _expect("k_prefix", k_prefix, q, (Bp, Hkv, P, d), q.dtype)
+        if v_prefix is None:
+            raise ValueError("v_prefix is required with k_prefix")
+        _expect("v_prefix", v_prefix, q, (Bp, Hkv, P, d), q.dtype)
+        _expect("prefix_len", prefix_len, q, (Bp,), torch.int32)
+    elif v_prefix is not None or prefix_len is not None:
+        raise ValueError("v_prefix and prefix_len need k_prefix")
+    if k_cache is not None:
+        _, Hc, C, _ = _shape4("k_cache", k_cache)
+        Hkv = Hkv or Hc
+        _expect("k_cache", k_cache, q, (B, Hkv, C, d), q.dtype)
+        if v_cache is None:
+            raise ValueError("v_cache is required with k_cache")
+        _expect("v_cache", v_cache, q, (B, Hkv, C, d), q.dtype)
+        _expect("cache_len", cache_len, q, (B,), torch.int32)
+    elif v_cache is not None or cache_len is not None:
+        raise ValueError("v_cache and cache_len need k_cache")
+    need = psa_decode_workspace_size(B, Hq, Hkv, T, d, Bp, P, C)
+    if ws is None:
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    _expect("ws", ws, q, dtype=torch.uint8, min_numel=need)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _expect("out", out, q, (B, Hq, T, d), q.dtype)
+    if lse is None:
+        if want_lse:
+            lse = torch.empty(B, Hq, T, dtype=torch.float32, device=q.device)
+    else:
+        _expect("lse", lse, q, (B, Hq, T), torch.float32)
+    _call("psa_decode", q, _ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(prefix_len), _ptr(k_cache), _ptr(v_cache),
+          _ptr(cache_len), B, Hq, Hkv, T, d, Bp, P, C, dt, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
+          _stream(stream, q))
+    return (out, lse) if lse is not None else out
+
+
+def psa_cache_evict_workspace_size(B: int, Hkv: int, C: int, budget: int) -> int:
+    return int(lib().psa_cache_evict_workspace_size(B, Hkv, C, budget))
+
+
+def cache_evict_workspace(B, Hkv, C, budget, device=None) -> torch.Tensor:
+    """A device workspace of psa_cache_evict_workspace_size bytes."""
+    return _serve_ws("psa_cache_evict_workspace_size", psa_cache_evict_workspace_size(B, Hkv, C, budget), device)
+
+
+def psa_cache_evict(k, v, score, budget: int, pos=None, cache_len=None, sink: int = 0, recent: int = 0, ws=None,
+                    out=None, stream=None):
+    """Keeps min(cache_len, budget) entries of every (sequence, KV head) of a
+    cache k, v [B, Hkv, C, d]: those at positions below ``sink``, the
+    ``recent`` latest, and the ones of largest ``score`` (float32 [B, Hkv, C],
+    equal scores by slot).  Returns (k, v, score, pos, length, kept): the
+    caches [B, Hkv, budget, d], their scores and positions, the new lengths
+    [B] and kept [B, Hkv, budget], the slot each entry came from (-1 past the
+    length).  ``out`` gives these six buffers instead; with the inputs
+    themselves as the first four the eviction is in place."""
+    B, Hkv, C, d = _shape4("k", k)
+    _dtype16("k", k)
+    _expect("v", v, k, (B, Hkv, C, d), k.dtype)
+    _expect("score", score, k, (B, Hkv, C), torch.float32)
+    _expect("pos", pos, k, (B, Hkv, C), torch.int32)
+    _expect("cache_len", cache_len, k, (B,), torch.int32)
+    need = psa_cache_evict_workspace_size(B, Hkv, C, budget)
+    if ws is None:
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=k.device)
+    _expect("ws", ws, k, dtype=torch.uint8, min_numel=need)
+    if out is None:
+        if need == 0:
+            raise PSAError("psa_cache_evict", PSA_ERR_ARG if budget <= 0 else PSA_ERR_SHAPE)
+        new = lambda *s, dtype: torch.empty(*s, dtype=dtype, device=k.device)  # noqa: E731
+        out = (new(B, Hkv, budget, d, dtype=k.dtype), new(B, Hkv, budget, d, dtype=k.dtype),
+               new(B, Hkv, budget, dtype=torch.float32), new(B, Hkv, budget, dtype=torch.int32),
+               new(B, dtype=torch.int32), new(B, Hkv, budget, dtype=torch.int32))
+    k_out, v_out, score_out, pos_out, len_out, kept = out
+    C_out = _shape4("k_out", k_out)[2]
+    _expect("k_out", k_out, k, (B, Hkv, C_out, d), k.dtype)
+    _expect("v_out", v_out, k, (B, Hkv, C_out, d), k.dtype)
+    _expect("score_out", score_out, k, (B, Hkv, C_out), torch.float32)
+    _expect("pos_out", pos_out, k, (B, Hkv, C_out), torch.int32)
+    _expect("len_out", len_out, k, (B,), torch.int32)
+    _expect("kept", kept, k, (B, Hkv, budget), torch.int32)
+    _call("psa_cache_evict", k, _ptr(k), _ptr(v), _ptr(score), _ptr(pos), _ptr(cache_len), B, Hkv, C, d, budget,
+          sink, recent, C_out, _ptr(k_out), _ptr(v_out), _ptr(score_out), _ptr(pos_out), _ptr(len_out), _ptr(kept),
+          _ptr(ws), ws.numel(), _stream(stream, k))
+    return k_out, v_out, score_out, pos_out, len_out, kept
 
 
 def psa_test_stall_next_attn(on: bool = True) -> None:

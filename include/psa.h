@@ -62,8 +62,12 @@ enum psa_status {
     PSA_ERR_CUDA = 5,         /* a CUDA runtime / driver call failed           */
     PSA_ERR_TIMEOUT = 6,      /* device: a bounded wait ran out (kernel quit)   */
     PSA_ERR_CSR = 7,          /* device: a listed block is out of range or repeated */
-    PSA_ERR_DEVICE = 8        /* no sm_100 device current, or a tensor of another device */
+    PSA_ERR_DEVICE = 8,       /* no sm_100 device current, or a tensor of another device */
+    PSA_ERR_LENGTH = 9        /* device: a sequence length out of range (clamped) */
 };
+
+/* Element type of the serving operators' queries, keys, values and outputs. */
+enum psa_dtype { PSA_BF16 = 0, PSA_FP16 = 1 };
 
 /* Text for a status code (static storage, never NULL). */
 PSA_API const char* psa_status_string(int status);
@@ -305,6 +309,73 @@ PSA_API int psa_attn_noalloc(const psa_bf16_t* q, const psa_bf16_t* k, const psa
                              const int* row_ptr, const int* col_idx, size_t col_capacity,
                              const float* row_max, int B, int H, int N, int d, int block_size,
                              int causal, psa_bf16_t* out, float* lse, int* status, void* stream);
+
+/*
+ * ---------------------------------------------------------------- serving
+ * What follows a prefill: attention of new tokens over the keys and values it
+ * left, and keeping that cache within a budget.  (The method's sources stop
+ * at the prefill; these operators are written from the formulas below.)
+ * Shared conventions: 16-bit elements of one type `dtype` (psa_dtype) per
+ * call; Hq query heads in groups of G = Hq / Hkv per KV head (query head
+ * h reads KV head h / G); d in {64, 128}; caches are [.., Hkv, capacity, d]
+ * with capacity <= 2^20 and may pass 2^31 elements; valid lengths are device
+ * int32 arrays (NULL: the capacity), so that they may change between replays
+ * of a captured graph.  A length outside [0, capacity] is clamped and
+ * recorded as PSA_ERR_LENGTH in the workspace status word, which every call
+ * sets anew.  A call needs its own workspace (256-byte aligned) while its
+ * work is in flight; calls ordered on one stream may share one.
+ *
+ * Attention of T new tokens per sequence over a prefix shared by groups of
+ * sequences and each sequence's own cache, in one softmax:
+ *   q, out [B,Hq,T,d]; k_prefix, v_prefix [Bp,Hkv,P,d], prefix_len [Bp];
+ *   k_cache, v_cache [B,Hkv,C,d], cache_len [B].  B = Bp * n: sequence b
+ *   reads prefix b / n (its keys are read once for the n sequences) and its
+ *   own cache, whose last T valid entries are the new tokens themselves.
+ *   Query t sees prefix keys j < prefix_len and cache slots
+ *   j < cache_len - (T - 1 - t), in whatever order the slots are.
+ *   out_t = sum_j e^{s_tj} v_j / sum_j e^{s_tj},  s = q.k / sqrt(d)
+ *   lse[B,Hq,T] (float32, may be NULL) = ln sum_j e^{s_tj}
+ * A row that sees no key gives out = 0, lse = -inf.  Rows of K and V past a
+ * length may hold anything, NaN included; the new tokens' values must be
+ * finite (a masked one is multiplied by zero).  P = 0 (no prefix: its
+ * pointers NULL) or C = 0 (no caches), not both; T <= 256.
+ * Softmax terms are rounded to `dtype` for the tensor cores; sums and the
+ * combination of parts are float32.
+ * Errors: PSA_ERR_ARG, PSA_ERR_SHAPE (Hq % Hkv, B % Bp, sizes too big),
+ * PSA_ERR_UNSUPPORTED, PSA_ERR_CAPACITY, PSA_ERR_DEVICE, PSA_ERR_CUDA.
+ */
+PSA_API size_t psa_decode_workspace_size(int B, int Hq, int Hkv, int T, int d, int Bp, int P, int C);
+PSA_API int psa_decode(const void* q, const void* k_prefix, const void* v_prefix,
+                       const int* prefix_len, const void* k_cache, const void* v_cache,
+                       const int* cache_len, int B, int Hq, int Hkv, int T, int d, int Bp,
+                       int P, int C, int dtype, void* out, float* lse, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * Eviction: every (sequence, KV head) keeps nk = min(cache_len, budget)
+ * entries.  Entries rank: protected ones first (pos < sink, or among the
+ * `recent` latest positions: pos > max pos - recent), then by score
+ * descending (NaN lowest), equal scores by slot ascending; the first nk stay.
+ * Slots below nk whose entry stays keep it; the others, ascending, take the
+ * staying entries of the slots from nk on, ascending.
+ *   in:  k, v 16-bit [B,Hkv,C,d]; score float32 [B,Hkv,C]; pos int32
+ *        [B,Hkv,C], the token positions (NULL: the slot index); cache_len [B]
+ *   out: k_out, v_out [B,Hkv,C_out,d], score_out, pos_out [B,Hkv,C_out]
+ *        (slots from nk on left as they were), len_out [B] = nk,
+ *        kept int32 [B,Hkv,budget]: the slot each entry came from, -1 past nk
+ * In place: k_out, v_out, score_out, and pos_out where pos is given, are the
+ * inputs and C_out = C; then only the rows that change slot move.  len_out
+ * may be cache_len in either form.  Any other overlap is refused.
+ * sink + recent <= budget <= C, budget <= C_out.
+ * Errors: PSA_ERR_ARG, PSA_ERR_SHAPE, PSA_ERR_UNSUPPORTED, PSA_ERR_CAPACITY,
+ * PSA_ERR_DEVICE, PSA_ERR_CUDA.
+ */
+PSA_API size_t psa_cache_evict_workspace_size(int B, int Hkv, int C, int budget);
+PSA_API int psa_cache_evict(const void* k, const void* v, const float* score, const int* pos,
+                            const int* cache_len, int B, int Hkv, int C, int d, int budget,
+                            int sink, int recent, int C_out, void* k_out, void* v_out,
+                            float* score_out, int* pos_out, int* len_out, int* kept,
+                            void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Test hook for the failure path (the method's sources have no counterpart;
