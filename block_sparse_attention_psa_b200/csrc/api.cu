@@ -296,6 +296,15 @@ int check_decode_shape(int B, int Hq, int Hkv, int T, int d, int Bp, int P, int 
   return psa::decode_workspace_bytes(B, Hq / Hkv, Hkv, T, d, Bp, P, C) ? PSA_OK : PSA_ERR_SHAPE;
 }
 
+int check_weight_shape(int B, int Hq, int Hkv, int T, int d, int Bk, int C) {
+  const int s = check_serve(B, Hq, Hkv, d, PSA_BF16);
+  if (s != PSA_OK) return s;
+  if (T <= 0 || Bk <= 0 || C <= 0) return PSA_ERR_ARG;
+  if (T > kMaxCache || C > kMaxCache) return PSA_ERR_UNSUPPORTED;
+  if (B % Bk || static_cast<long long>(Hq / Hkv) * T >= (1LL << 31)) return PSA_ERR_SHAPE;
+  return psa::weight_workspace_bytes(B, Hq / Hkv, Hkv, T, Bk, C) ? PSA_OK : PSA_ERR_SHAPE;
+}
+
 int check_evict_shape(int B, int Hkv, int C, int budget) {
   if (B <= 0 || Hkv <= 0 || C <= 0 || budget <= 0) return PSA_ERR_ARG;
   if (C > kMaxCache) return PSA_ERR_UNSUPPORTED;
@@ -607,6 +616,51 @@ int psa_decode(const void* q, const void* k_prefix, const void* v_prefix, const 
   a.lse = lse;
   a.ws = static_cast<char*>(workspace);
   return cuda_status(psa::launch_decode(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t psa_key_weight_workspace_size(int B, int Hq, int Hkv, int T, int d, int Bk, int C) {
+  if (check_weight_shape(B, Hq, Hkv, T, d, Bk, C) != PSA_OK) return 0;
+  return psa::weight_workspace_bytes(B, Hq / Hkv, Hkv, T, Bk, C);
+}
+
+int psa_key_weight(const void* q, const void* k, const float* lse, const int* key_len, const float* score_in, int B,
+                   int Hq, int Hkv, int T, int d, int Bk, int C, int causal, int dtype, float* score_out,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !k || !lse || !score_out || !workspace) return PSA_ERR_ARG;
+  int s = check_serve(B, Hq, Hkv, d, dtype);
+  if (s == PSA_OK) s = check_weight_shape(B, Hq, Hkv, T, d, Bk, C);
+  if (s != PSA_OK) return s;
+  if (causal != 0 && causal != 1) return PSA_ERR_ARG;
+  if (misaligned(q, 16) || misaligned(k, 16) || misaligned(lse, 4) || misaligned(key_len, 4) ||
+      misaligned(score_in, 4) || misaligned(score_out, 4) || misaligned(workspace, 256))
+    return PSA_ERR_ARG;
+  const size_t need = psa::weight_workspace_bytes(B, Hq / Hkv, Hkv, T, Bk, C);
+  if (workspace_bytes < need) return PSA_ERR_CAPACITY;
+  const size_t rows = static_cast<size_t>(B) * Hq * T, slots = static_cast<size_t>(Bk) * Hkv * C;
+  const Range out = {score_out, slots * 4};
+  if (overlap(out, {q, rows * d * 2}) || overlap(out, {k, slots * d * 2}) || overlap(out, {lse, rows * 4}) ||
+      (key_len && overlap(out, {key_len, static_cast<size_t>(Bk) * 4})) || overlap(out, {workspace, need}) ||
+      (score_in != score_out && overlap(out, {score_in, slots * 4})))
+    return PSA_ERR_ARG;
+  if ((s = check_device({q, k, lse, key_len, score_in, score_out, workspace})) != PSA_OK) return s;
+  psa::WeightLaunch a = {};
+  a.q = q;
+  a.k = k;
+  a.lse = lse;
+  a.key_len = key_len;
+  a.score_in = score_in;
+  a.score_out = score_out;
+  a.B = B;
+  a.G = Hq / Hkv;
+  a.Hkv = Hkv;
+  a.T = T;
+  a.d = d;
+  a.Bk = Bk;
+  a.C = C;
+  a.causal = causal;
+  a.fp16 = dtype == PSA_FP16;
+  a.ws = static_cast<char*>(workspace);
+  return cuda_status(psa::launch_weight(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t psa_cache_evict_workspace_size(int B, int Hkv, int C, int budget) {

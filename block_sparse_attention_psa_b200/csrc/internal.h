@@ -185,6 +185,21 @@ struct DecodeLaunch {
 size_t decode_workspace_bytes(int B, int G, int Hkv, int T, int d, int Bp, int P, int C);
 cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t st);
 
+// weight.cu: accumulated attention weight per cached key
+struct WeightLaunch {
+  const void* q;          // [B, Hkv * G, T, d]
+  const void* k;          // [Bk, Hkv, C, d]
+  const float* lse;       // [B, Hkv * G, T]
+  const int* key_len;     // [Bk], null: C
+  const float* score_in;  // [Bk, Hkv, C], nullable
+  float* score_out;       // [Bk, Hkv, C]
+  int B, G, Hkv, T, d, Bk, C, causal;
+  bool fp16;
+  char* ws;
+};
+size_t weight_workspace_bytes(int B, int G, int Hkv, int T, int Bk, int C);  // 0: too large to schedule
+cudaError_t launch_weight(const WeightLaunch& a, cudaStream_t st);
+
 // evict.cu: eviction from a cache by accumulated weight
 struct EvictLaunch {
   const void* k;        // 16-bit [B, Hkv, C, d]

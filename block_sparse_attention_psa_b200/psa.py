@@ -37,7 +37,8 @@ EXPORTS = ("psa_status_string", "psa_version", "psa_workspace_size", "psa_route_
            "psa_route_topk", "psa_route_thresh", "psa_attn", "psa_dense", "psa_read_status",
            "psa_attn_noalloc", "psa_route_thresh_prob", "psa_test_stall_next_attn",
            "psa_read_fixup_count", "psa_hyd_stat", "psa_attn_hyd", "psa_attn_bwd", "psa_decode_workspace_size",
-           "psa_decode", "psa_cache_evict_workspace_size", "psa_cache_evict")
+           "psa_decode", "psa_key_weight_workspace_size", "psa_key_weight", "psa_cache_evict_workspace_size",
+           "psa_cache_evict")
 
 _lib = None
 
@@ -68,6 +69,8 @@ def _declare(L: ctypes.CDLL) -> None:
         "psa_attn_hyd": (I, [P, P, P, P, P, P, P, P, Z, P, I, I, I, I, I, I, P, P, P, Z, P]),
         "psa_decode_workspace_size": (Z, [I] * 8),
         "psa_decode": (I, [P] * 7 + [I] * 9 + [P, P, P, Z, P]),
+        "psa_key_weight_workspace_size": (Z, [I] * 7),
+        "psa_key_weight": (I, [P] * 5 + [I] * 9 + [P, P, Z, P]),
         "psa_cache_evict_workspace_size": (Z, [I] * 4),
         "psa_cache_evict": (I, [P] * 5 + [I] * 8 + [P] * 7 + [Z, P]),
         "psa_test_stall_next_attn": (I, [I]),
@@ -486,6 +489,44 @@ def psa_decode(q, k_cache=None, v_cache=None, cache_len=None, k_prefix=None, v_p
           _ptr(cache_len), B, Hq, Hkv, T, d, Bp, P, C, dt, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
           _stream(stream, q))
     return (out, lse) if lse is not None else out
+
+
+def psa_key_weight_workspace_size(B: int, Hq: int, Hkv: int, T: int, d: int, Bk: int, C: int) -> int:
+    return int(lib().psa_key_weight_workspace_size(B, Hq, Hkv, T, d, Bk, C))
+
+
+def key_weight_workspace(B, Hq, Hkv, T, d, Bk, C, device=None) -> torch.Tensor:
+    """A device workspace of psa_key_weight_workspace_size bytes."""
+    return _serve_ws("psa_key_weight_workspace_size", psa_key_weight_workspace_size(B, Hq, Hkv, T, d, Bk, C), device)
+
+
+def psa_key_weight(q, k, lse, key_len=None, causal: bool = False, score=None, ws=None, out=None, stream=None):
+    """Accumulated attention weight of each cached key, float32 [Bk, Hkv, C]:
+    ``score`` (None: zero) plus, per slot j of k [Bk, Hkv, C, d], the sum of
+    exp(q . k_j / sqrt(d) - lse) over the queries q [B, Hq, T, d] that see it
+    (groups of B / Bk sequences read one key set; causal: token t sees slots
+    below key_len - (T - 1 - t)).  Slots past ``key_len`` get 0.  ``out`` may
+    be ``score`` itself."""
+    B, Hq, T, d = _shape4("q", q)
+    dt = _dtype16("q", q)
+    Bk, Hkv, C, _ = _shape4("k", k)
+    _expect("k", k, q, (Bk, Hkv, C, d), q.dtype)
+    if lse is None:
+        raise ValueError("lse (float32 [B, Hq, T]) of the queries is required")
+    _expect("lse", lse, q, (B, Hq, T), torch.float32)
+    _expect("key_len", key_len, q, (Bk,), torch.int32)
+    _expect("score", score, q, (Bk, Hkv, C), torch.float32)
+    need = psa_key_weight_workspace_size(B, Hq, Hkv, T, d, Bk, C)
+    if ws is None:
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    _expect("ws", ws, q, dtype=torch.uint8, min_numel=need)
+    if out is None:
+        out = torch.empty(Bk, Hkv, C, dtype=torch.float32, device=q.device)
+    else:
+        _expect("out", out, q, (Bk, Hkv, C), torch.float32)
+    _call("psa_key_weight", q, _ptr(q), _ptr(k), _ptr(lse), _ptr(key_len), _ptr(score), B, Hq, Hkv, T, d, Bk, C,
+          int(causal), dt, _ptr(out), _ptr(ws), ws.numel(), _stream(stream, q))
+    return out
 
 
 def psa_cache_evict_workspace_size(B: int, Hkv: int, C: int, budget: int) -> int:

@@ -352,6 +352,31 @@ PSA_API int psa_decode(const void* q, const void* k_prefix, const void* v_prefix
                        size_t workspace_bytes, void* stream);
 
 /*
+ * Accumulated attention weight of each cached key (the column sums of the
+ * softmax matrix, recomputed from the queries' lse):
+ *   score_out[bk,h,j] = score_in[bk,h,j] + sum over the sequences b of key
+ *     set bk, the query heads of KV head h and the tokens t that see slot j
+ *     of e^{q.k_j / sqrt(d) - lse[b,hq,t]}             (j < key_len)
+ *   score_out[bk,h,j] = 0                              (j >= key_len)
+ *   q [B,Hq,T,d]; k [Bk,Hkv,C,d]; lse float32 [B,Hq,T] as psa_decode,
+ *   psa_dense or psa_attn give it (-inf: the query adds nothing); key_len
+ *   [Bk]; B = Bk * n, sequence b reads key set b / n.  Token t sees slot j
+ *   iff causal = 0, or j < key_len - (T - 1 - t) (the last T entries are the
+ *   tokens themselves: T = key_len is a causal prefill, a small T an
+ *   observation window or a decode step).
+ * score_in may be NULL (zero) or score_out itself (accumulate in place); any
+ * other overlap of score_out is refused.  T, C <= 2^20.  Sums are float32,
+ * in a fixed order.
+ * Errors: PSA_ERR_ARG, PSA_ERR_SHAPE, PSA_ERR_UNSUPPORTED, PSA_ERR_CAPACITY,
+ * PSA_ERR_DEVICE, PSA_ERR_CUDA.
+ */
+PSA_API size_t psa_key_weight_workspace_size(int B, int Hq, int Hkv, int T, int d, int Bk, int C);
+PSA_API int psa_key_weight(const void* q, const void* k, const float* lse, const int* key_len,
+                           const float* score_in, int B, int Hq, int Hkv, int T, int d, int Bk,
+                           int C, int causal, int dtype, float* score_out, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
  * Eviction: every (sequence, KV head) keeps nk = min(cache_len, budget)
  * entries.  Entries rank: protected ones first (pos < sink, or among the
  * `recent` latest positions: pos > max pos - recent), then by score
