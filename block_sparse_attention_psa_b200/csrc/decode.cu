@@ -15,17 +15,21 @@
 //    products S = Q K^T (Q, K in shared memory) and O += P V (P in TMEM,
 //    written over S; V MN-major in shared memory).  An unfilled tile costs
 //    tensor time, which few rows leave idle.
-//  * Streams.  A CTA runs two softmax warpgroups, each with its own S/P and O
-//    in TMEM (512 columns in all).  With two row tiles or more each takes one
-//    of a pair, so that K and V are read once for 256 rows; with one row tile
+//  * Streams.  A CTA runs two softmax streams, each with its own S/P and O in
+//    TMEM (512 columns in all).  With two row tiles or more each takes one of
+//    a pair, so that K and V are read once for 256 rows; with one row tile
 //    they take alternate key tiles and give two parts.  Items go to the
 //    streams in turn, one thread issues every product: PV of the item two
 //    back, then S of this one, so that one stream's softmax covers the other's
-//    products.
+//    products.  A stream is a chain S -> softmax -> PV -> S (P lies over S and
+//    TMEM has no room for a second); the PV product of a tile's first 64 keys
+//    starts when their half of P is there.
 //  * Split.  The key tiles of all units (KV head x row-tile pair) are laid
-//    out in one line, the prefixes first, and cut into equal runs, one per
-//    SM: every SM reads the same number of tiles whatever the lengths, which
-//    live on the device.  A unit's run in one CTA is a piece; its parts
+//    out in two lines, the prefixes' and the caches', a tile for a pair twice
+//    as long, and each line is cut into equal runs, one per SM, whatever the
+//    lengths, which live on the device.  (One line for both left the SMs that
+//    got the caches, short units with a load and a part each, twice as long at
+//    work as the others.)  A unit's run in one CTA is a piece; its parts
 //    (running maximum, sum and unnormalised O, fp32) go to the workspace.
 //  * Stabiliser.  A row's reference exponent only moves when a tile's maximum
 //    passes it by 2^8, so O is rarely rescaled, and terms stay below 2^8.
@@ -75,7 +79,7 @@ struct Params {
   int own_rb, own_rt, own_up;
   float scale_log2;
   long long pre_slots; // slots of the prefix region: the caches' parts start behind it
-  long long* seg_off;  // [nseg + 1] first tile of each segment
+  long long* seg_off;  // [npre + 1] and [caches + 1]: first place of each segment on its line, then the line's length
   float* part_o;       // parts: rows x d
   float2* part_ml;     // reference (log2 units), sum
   int* status;
@@ -102,7 +106,16 @@ __device__ __forceinline__ bool seg_bad(const Params& p, int s) {
   if (s < p.npre) return p.prefix_len && (p.prefix_len[s] < 0 || p.prefix_len[s] > p.P);
   return p.cache_len && (p.cache_len[s - p.npre] < 0 || p.cache_len[s - p.npre] > p.C);
 }
-__device__ __forceinline__ int seg_units(const Params& p, int s) { return p.Hkv * (s < p.npre ? p.pre_up : p.own_up); }
+// Length of a segment on the line: its row tiles times its key tiles (the
+// last unit of a KV head has one row tile when their number is odd).
+__device__ __forceinline__ long long seg_work(const Params& p, int s) {
+  return static_cast<long long>((seg_len(p, s) + 127) / 128) * p.Hkv * (s < p.npre ? p.pre_rt : p.own_rt);
+}
+// Key tiles of a unit (from `o` on the line, w = 1 or 2 per tile) before x:
+// a cut inside a tile leaves it to the run it starts in.
+__device__ __forceinline__ long long tiles_before(long long x, long long o, int w) {
+  return w == 1 ? x - o : (x - o + 1) >> 1;
+}
 
 __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
   const long long t0 = clock64();
@@ -118,6 +131,21 @@ __device__ __forceinline__ void reg_dealloc() {
 template <int N>
 __device__ __forceinline__ void reg_alloc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+
+// Terms of 64 keys of one row, 2^(s * scale + neg), packed to the input type,
+// with their sum.
+template <bool FP16>
+__device__ __forceinline__ void exps(const float* v, float scale, float neg, float (&l)[4], uint32_t (&pk)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    float x0, x1;
+    ffma2(x0, x1, v[2 * i], v[2 * i + 1], scale, scale, neg, neg);
+    x0 = ex2_approx(x0);
+    x1 = ex2_approx(x1);
+    fadd2(l[2 * (i & 1)], l[2 * (i & 1) + 1], l[2 * (i & 1)], l[2 * (i & 1) + 1], x0, x1);
+    pk[i] = pack_16x2<FP16>(x0, x1);
+  }
 }
 
 template <int D, bool FP16>
@@ -140,16 +168,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_full = bars + 12;   // [kSt]
   uint64_t* v_empty = bars + 16;  // [kSt] last PV product of the tile  (commit)
   uint64_t* s_full = bars + 20;   // [2] S of the stream ready          (commit)
-  uint64_t* p_full = bars + 22;   // [2] P written over it              (4 warps)
-  uint64_t* o_full = bars + 24;   // [2] last PV of the piece done      (commit)
-  uint64_t* pc_full = bars + 26;  // [kRing] a piece published
-  uint64_t* pc_empty = bars + 30; // [kRing] read by V loads, MMA issue, 8 softmax warps
-  uint64_t* drain = bars + 34;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc + 288);
+  uint64_t* p_full = bars + 22;   // [2][2] half of P written over it   (4 warps)
+  uint64_t* o_full = bars + 26;   // [2] last PV of the piece done      (commit)
+  uint64_t* pc_full = bars + 28;  // [kRing] a piece published
+  uint64_t* pc_empty = bars + 32; // [kRing] read by V loads, MMA issue, 8 softmax warps
+  uint64_t* drain = bars + 36;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc + 320);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* start_seg = reinterpret_cast<int*>(tmem_slot + 2);
-  long long* start_off = reinterpret_cast<long long*>(smem + C::kOffMisc + 304);  // first tile of start_seg
-  long long* red = start_off + 1;                                                 // [12 + 1]
+  int* start_seg = reinterpret_cast<int*>(tmem_slot + 2);                         // [2] where the runs start,
+  long long* start_off = reinterpret_cast<long long*>(smem + C::kOffMisc + 336);  // [2] and its place on the line
+  long long* red = start_off + 2;                                                 // [20]
   volatile int* ring = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 512); // [kRing][kPieceInts]
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -158,7 +186,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[2 * i], 4);
+      mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&o_full[i], 1);
     }
     for (int i = 0; i < kSt; ++i) {
@@ -173,8 +202,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
-    *start_seg = p.nseg;
-    *start_off = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -196,31 +223,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_launch();
   grid_dep_wait();
 
-  // ---- schedule: total tiles, then the segment in which this CTA's run starts
-  long long mine = 0;
+  // ---- schedule: the lines' lengths, then where this CTA's runs start
+  long long x0[2], x1[2];
   bool bad = false;
-  for (int s = threadIdx.x; s < p.nseg; s += kThreads) {
-    mine += static_cast<long long>((seg_len(p, s) + 127) / 128) * seg_units(p, s);
-    bad |= blockIdx.x == 0 && seg_bad(p, s);
-  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) red[warp] = mine;
-  bad = __syncthreads_or(bad);
-  long long total = 0;
+  for (int line = 0; line < 2; ++line) {
+    const int sa = line ? p.npre : 0, sb = line ? p.nseg : p.npre;
+    long long mine = 0;
+    for (int s = sa + threadIdx.x; s < sb; s += kThreads) {
+      mine += seg_work(p, s);
+      bad |= blockIdx.x == 0 && seg_bad(p, s);
+    }
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) total += red[w];
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    *p.status = bad ? kStatusLength : 0;  // the call's first write of the status word
-    p.seg_off[p.nseg] = total;
-  }
-  const long long x0 = total * blockIdx.x / gridDim.x, x1 = total * (blockIdx.x + 1) / gridDim.x;
-  if (x0 < x1 || blockIdx.x == 0) {
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    __syncthreads();
+    if (lane == 0) red[warp] = mine;
+    __syncthreads();
+    long long total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) total += red[w];
+    x0[line] = total * blockIdx.x / gridDim.x;
+    x1[line] = total * (blockIdx.x + 1) / gridDim.x;
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.seg_off[sb + line] = total;
     long long run = 0;
-    for (int s0 = 0; s0 < p.nseg; s0 += kThreads) {
+    for (int s0 = sa; s0 < sb && (x0[line] < x1[line] || blockIdx.x == 0); s0 += kThreads) {
       const int s = s0 + threadIdx.x;
-      const long long t =
-          s < p.nseg ? static_cast<long long>((seg_len(p, s) + 127) / 128) * seg_units(p, s) : 0;
+      const long long t = s < sb ? seg_work(p, s) : 0;
       long long inc = t;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -236,47 +263,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         run += red[w];
       }
       const long long lo = base + inc - t, hi = base + inc;
-      if (lo <= x0 && x0 < hi) {
-        *start_seg = s;
-        *start_off = lo;
+      if (lo <= x0[line] && x0[line] < hi) {
+        start_seg[line] = s;
+        start_off[line] = lo;
       }
-      if (blockIdx.x == 0 && s < p.nseg) p.seg_off[s] = lo;
+      if (blockIdx.x == 0 && s < sb) p.seg_off[s + line] = lo;
     }
   }
-  __syncthreads();
+  bad = __syncthreads_or(bad);
+  // the call's first write of the status word
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = bad ? kStatusLength : 0;
 
   if (warp < 4) {
     reg_dealloc<kRegsProducer>();
     if (warp == 0) {
       // ---------------------------------------------------- scheduler, Q and K loads
-      long long x = x0, off = *start_off;
-      int s = *start_seg;
       int tiles = 0, items = 0, qpos = 0, np = 0, kl = 0, ql = 0;
       bool ok = true;
+      for (int turn = 0; turn < 2; ++turn) {
+      const int line = turn;
+      long long x = line ? x0[1] : x0[0], off = start_off[line];
+      const long long xe = line ? x1[1] : x1[0];
+      int s = start_seg[line];
       int lens = 0, lens0 = -64;  // lane l holds the length of segment lens0 + l
-      while (ok && x < x1) {
+      while (ok && x < xe) {
         if (s - lens0 >= 32) {
           lens0 = s;
           lens = s + lane < p.nseg ? seg_len(p, s + lane) : 0;
         }
         const int len = __shfl_sync(0xffffffffu, lens, s - lens0);
         const int nkt = (len + 127) / 128;
-        const long long here = static_cast<long long>(nkt) * seg_units(p, s);
+        const bool pre = s < p.npre;
+        const int up = pre ? p.pre_up : p.own_up, rt = pre ? p.pre_rt : p.own_rt;
+        const long long per_head = static_cast<long long>(nkt) * rt, here = per_head * p.Hkv;
         if (x >= off + here) {
           off += here;
           ++s;
           continue;
         }
         Piece c;
-        const int lu = static_cast<int>((x - off) / nkt);
-        c.prefix = s < p.npre;
-        c.outer = c.prefix ? s : s - p.npre;
-        const int up = c.prefix ? p.pre_up : p.own_up, rt = c.prefix ? p.pre_rt : p.own_rt;
-        c.hkv = lu / up;
-        c.tile0 = 2 * (lu - c.hkv * up);
+        c.prefix = pre;
+        c.outer = pre ? s : s - p.npre;
+        c.hkv = static_cast<int>((x - off) / per_head);
+        const long long head0 = off + c.hkv * per_head;
+        const int u = static_cast<int>((x - head0) / (2 * nkt));  // every unit before the last is a pair
+        const int lu = c.hkv * up + u;
+        c.tile0 = 2 * u;
         c.pair = c.tile0 + 1 < rt;
-        c.j0 = static_cast<int>(x - off - static_cast<long long>(lu) * nkt);
-        c.nt = static_cast<int>(min(static_cast<long long>(nkt - c.j0), x1 - x));
+        const long long o0 = head0 + 2LL * u * nkt, o1 = o0 + static_cast<long long>(nkt) * (1 + c.pair);
+        c.j0 = static_cast<int>(tiles_before(x, o0, 1 + c.pair));
+        c.nt = static_cast<int>(tiles_before(min(o1, xe), o0, 1 + c.pair)) - c.j0;
+        x = min(o1, xe);
+        if (c.nt == 0) continue;  // the rest of a tile that the run before took
         c.len = len;
         c.slot = c.outer * p.Hkv * up + lu + static_cast<int>(blockIdx.x);
         c.tiles = tiles;
@@ -284,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         c.qpos = qpos;
         if (lane == 0) {
           const int slot = np % kRing;
-          if (np >= kRing) ok = mbar_wait(&pc_empty[slot], ((np / kRing) - 1) & 1, abort_flag, p.status);
+          if (np >= kRing) ok = mbar_sleep(&pc_empty[slot], ((np / kRing) - 1) & 1, abort_flag, p.status);
           if (ok) {
             const int* w = reinterpret_cast<const int*>(&c);
             for (int i = 0; i < kPieceInts; ++i) ring[slot * kPieceInts + i] = w[i];
@@ -294,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const CUtensorMap* mq = c.prefix ? &tmQp : &tmQc;
           for (int i = 0; i <= c.pair && ok; ++i) {
             const int qs = (qpos + i) & 1, n = (qpos + i) >> 1;
-            ok = mbar_wait(&q_empty[qs], (n & 1) ^ 1, abort_flag, p.status);
+            ok = mbar_sleep(&q_empty[qs], (n & 1) ^ 1, abort_flag, p.status);
             if (!ok) break;
             const int tile = c.tile0 + i;
             int r = 0, b;
@@ -323,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const CUtensorMap* mk = c.prefix ? &tmKp : &tmKc;
           for (int j = 0; j < c.nt && ok; ++j) {
             const int st = (tiles + j) % kSt, n = (tiles + j) / kSt;
-            ok = mbar_wait(&k_empty[st], (n & 1) ^ 1, abort_flag, p.status);
+            ok = mbar_sleep(&k_empty[st], (n & 1) ^ 1, abort_flag, p.status);
             if (!ok) break;
             const int y = 128 * (c.j0 + j);
             const int halves = c.len - y > 64 ? 2 : 1;
@@ -340,13 +378,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tiles += c.nt;
         items += c.pair ? 2 * c.nt : c.nt;
         qpos += 1 + c.pair;
-        x += c.nt;
         ++np;
+      }
       }
       if (lane == 0) {
         // the end mark: a piece without tiles
         const int slot = np % kRing;
-        if (ok && np >= kRing) ok = mbar_wait(&pc_empty[slot], ((np / kRing) - 1) & 1, abort_flag, p.status);
+        if (ok && np >= kRing) ok = mbar_sleep(&pc_empty[slot], ((np / kRing) - 1) & 1, abort_flag, p.status);
         if (ok) {
           for (int i = 0; i < kPieceInts; ++i) ring[slot * kPieceInts + i] = 0;
           mbar_arrive(&pc_full[slot]);
@@ -356,113 +394,135 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = max(0, ql - 2); t < ql; ++t) mbar_drain(&q_full[t & 1], (t >> 1) & 1);
       }
       __syncwarp();
-    } else if (lane == 0 && (warp == 1 || warp == 2)) {
-      // reads the next piece; false at the end or on a timeout
-      int np = 0;
-      auto next = [&](Piece& c) -> bool {
+    } else if (warp == 2 && lane == 0) {
+      // ---------------------------------------------------- V loads
+      int np = 0, vl = 0;
+      bool ok = true;
+      while (ok) {
         const int slot = np % kRing;
-        if (!mbar_wait(&pc_full[slot], (np / kRing) & 1, abort_flag, p.status)) return false;
+        if (!(ok = mbar_sleep(&pc_full[slot], (np / kRing) & 1, abort_flag, p.status))) break;
+        Piece c;
         int* w = reinterpret_cast<int*>(&c);
         for (int i = 0; i < kPieceInts; ++i) w[i] = ring[slot * kPieceInts + i];
         mbar_arrive(&pc_empty[slot]);
         ++np;
-        return c.nt > 0;
-      };
-      if (warp == 2) {
-        // -------------------------------------------------- V loads
-        Piece c;
-        int vl = 0;
-        bool ok = true;
-        while (ok && next(c)) {
-          const CUtensorMap* mv = c.prefix ? &tmVp : &tmVc;
-          for (int j = 0; j < c.nt; ++j) {
-            const int st = (c.tiles + j) % kSt, n = (c.tiles + j) / kSt;
-            if (!(ok = mbar_wait(&v_empty[st], (n & 1) ^ 1, abort_flag, p.status))) break;
-            const int y = 128 * (c.j0 + j);
-            const int halves = c.len - y > 64 ? 2 : 1;
-            mbar_arrive_expect_tx(&v_full[st], halves * 64 * 128 * C::kChunks);
-            for (int h = 0; h < halves; ++h)
+        if (c.nt == 0) break;
+        const CUtensorMap* mv = c.prefix ? &tmVp : &tmVc;
+        for (int j = 0; j < c.nt; ++j) {
+          const int st = (c.tiles + j) % kSt, n = (c.tiles + j) / kSt;
+          if (!(ok = mbar_sleep(&v_empty[st], (n & 1) ^ 1, abort_flag, p.status))) break;
+          const int y = 128 * (c.j0 + j);
+          const int halves = c.len - y > 64 ? 2 : 1;
+          mbar_arrive_expect_tx(&v_full[st], halves * 64 * 128 * C::kChunks);
+          for (int h = 0; h < halves; ++h)
 #pragma unroll
-              for (int ch = 0; ch < C::kChunks; ++ch)
-                tma_load_3d(mv, sV + st * C::kTile + ch * 16384 + h * 8192, &v_full[st], 64 * ch, y + 64 * h,
-                            c.outer * p.Hkv + c.hkv);
-            vl = c.tiles + j + 1;
-          }
+            for (int ch = 0; ch < C::kChunks; ++ch)
+              tma_load_3d(mv, sV + st * C::kTile + ch * 16384 + h * 8192, &v_full[st], 64 * ch, y + 64 * h,
+                          c.outer * p.Hkv + c.hkv);
+          vl = c.tiles + j + 1;
         }
-        for (int t = max(0, vl - kSt); t < vl; ++t) mbar_drain(&v_full[t % kSt], (t / kSt) & 1);
-      } else {
-        // -------------------------------------------------- MMA issue
-        constexpr uint32_t kIdescS = idesc_f16_f32(FP16, 128, 128, 0, 0);
-        constexpr uint32_t kIdescO = idesc_f16_f32(FP16, 128, D, 0, 1);
-        const uint64_t dQ0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
-        const uint64_t dK0 = sdesc_sw128(smem_u32(sK), 16, 1024);
-        // V is read MN-major: 64-feature atoms 16 KB apart (d = 64: one atom)
-        const uint64_t dV0 = sdesc_sw128(smem_u32(sV), D == 128 ? 16384 : 0, 1024);
-        constexpr uint64_t kStep = C::kTile >> 4;
-        int cnt = 0;                   // items issued
-        int pv_tile[2] = {-1, -1};     // the PV product due on each stream: its tile,
-        uint32_t pv_flags[2] = {0, 0}; // 1: adds to O, 2: last of its tile, 4: last of its piece
-        int pv_n[2] = {0, 0};
-        bool ok = true;
-        auto issue_pv = [&](int s) -> bool {
-          const int t = s ? pv_tile[1] : pv_tile[0];
-          if (t < 0) return true;
-          const uint32_t f = s ? pv_flags[1] : pv_flags[0];
-          const int n = s ? pv_n[1] : pv_n[0];
-          const int st = t % kSt;
-          if (!mbar_wait(&p_full[s], n & 1, abort_flag, p.status)) return false;
-          if (!mbar_wait(&v_full[st], (t / kSt) & 1, abort_flag, p.status)) return false;
-          tc_fence_after();
-          const uint32_t a = tbase + 128 * s, o = tbase + 256 + D * s;
-          const uint64_t b = dV0 + st * kStep;
+      }
+      for (int t = max(0, vl - kSt); t < vl; ++t) mbar_drain(&v_full[t % kSt], (t / kSt) & 1);
+    } else if (warp == 1) {
+      // ---------------------------------------------------- MMA issue
+      // The whole warp walks the items in step; one elected lane issues.
+      constexpr uint32_t kIdescS = idesc_f16_f32(FP16, 128, 128, 0, 0);
+      constexpr uint32_t kIdescO = idesc_f16_f32(FP16, 128, D, 0, 1);
+      const uint64_t dQ0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t dK0 = sdesc_sw128(smem_u32(sK), 16, 1024);
+      // V is read MN-major: 64-feature atoms 16 KB apart (d = 64: one atom)
+      const uint64_t dV0 = sdesc_sw128(smem_u32(sV), D == 128 ? 16384 : 0, 1024);
+      constexpr uint64_t kStep = C::kTile >> 4;
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_sleep(bar, parity, abort_flag, p.status));
+      };
+      int np = 0, cnt = 0;         // pieces read, items issued
+      int t = 0;                   // running key tile
+      // the PV products due, of the items cnt - 2 and cnt - 1: tile and
+      // 1: adds to O, 2: last of its tile, 4: last of its piece on the stream
+      int t2 = -1, t1 = -1;
+      uint32_t f2 = 0, f1 = 0;
+      bool ok = true;
+      // Inside an item the lanes wait without a vote (a product issued after a
+      // wait that ran out reads stale operands, and its result is dropped);
+      // they agree on stopping once per item.
+      auto issue_pv = [&](int item, int tile, uint32_t f) -> bool {
+        const int s = item & 1, st = tile % kSt;
+        const uint32_t ph = (item >> 1) & 1, vh = (tile / kSt) & 1;
+        // one look at both barriers, whose latencies then overlap
+        const bool pr = mbar_try_wait(&p_full[2 * s], ph), vr = mbar_try_wait(&v_full[st], vh);
+        bool good = vr || mbar_sleep(&v_full[st], vh, abort_flag, p.status);
+        good &= pr || mbar_sleep(&p_full[2 * s], ph, abort_flag, p.status);
+        __syncwarp();
+        tc_fence_after();
+        const uint32_t a = tbase + 128 * s, o = tbase + 256 + D * s;
+        const uint64_t b = dV0 + st * kStep;
+        const uint32_t add = f & 1u;
+        if (elect_one()) {
+          tc_mma_f16_ts(o, a, b, kIdescO, add);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc_mma_f16_ts(o, a + 8 * kk, b + 128 * kk, kIdescO, kk ? 1u : (f & 1u));
+          for (int kk = 1; kk < 4; ++kk) tc_mma_f16_ts(o, a + 8 * kk, b + 128 * kk, kIdescO, 1u);
+        }
+        __syncwarp();
+        good &= mbar_sleep(&p_full[2 * s + 1], (item >> 1) & 1, abort_flag, p.status);
+        __syncwarp();
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 4; kk < 8; ++kk) tc_mma_f16_ts(o, a + 8 * kk, b + 128 * kk, kIdescO, 1u);
           if (f & 2u) tc_commit(&v_empty[st]);
           if (f & 4u) tc_commit(&o_full[s]);
-          if (s) {
-            ++pv_n[1];
-            pv_tile[1] = -1;
-          } else {
-            ++pv_n[0];
-            pv_tile[0] = -1;
-          }
-          return true;
-        };
-        Piece c;
-        while (ok && next(c)) {
-          const int ni = c.pair ? 2 * c.nt : c.nt;
-          for (int i = 0; i < ni; ++i, ++cnt) {
-            const int s = cnt & 1;
-            const int j = c.pair ? i >> 1 : i;
-            const int t = c.tiles + j, st = t % kSt;
-            const int q = c.qpos + (c.pair ? (i & 1) : 0), qs = q & 1;
-            if (!(ok = issue_pv(s))) break;
-            if (i <= c.pair && !(ok = mbar_wait(&q_full[qs], (q >> 1) & 1, abort_flag, p.status))) break;
-            if (!(ok = mbar_wait(&k_full[st], (t / kSt) & 1, abort_flag, p.status))) break;
-            tc_fence_after();
-            const uint64_t a = dQ0 + qs * kStep, b = dK0 + st * kStep;
+        }
+        __syncwarp();
+        return good;
+      };
+      while (ok) {
+        const int slot = np % kRing;
+        if (!(ok = wait(&pc_full[slot], (np / kRing) & 1))) break;
+        const volatile Piece* c = reinterpret_cast<volatile Piece*>(ring + slot * kPieceInts);
+        const int nt = __shfl_sync(0xffffffffu, c->nt, 0), pair = __shfl_sync(0xffffffffu, c->pair, 0);
+        const int qpos = __shfl_sync(0xffffffffu, c->qpos, 0);
+        __syncwarp();
+        if (elect_one()) mbar_arrive(&pc_empty[slot]);
+        ++np;
+        if (nt == 0) break;
+        const int ni = pair ? 2 * nt : nt;
+        for (int i = 0; i < ni; ++i) {
+          const int s = cnt & 1, st = t % kSt;
+          const int q = qpos + (i & pair), qs = q & 1;
+          const uint32_t kh = (t / kSt) & 1;
+          const bool kr = mbar_try_wait(&k_full[st], kh);
+          if (t2 >= 0) ok = issue_pv(cnt - 2, t2, f2);
+          if (i <= pair) ok &= mbar_sleep(&q_full[qs], (q >> 1) & 1, abort_flag, p.status);
+          if (!kr) ok &= mbar_sleep(&k_full[st], kh, abort_flag, p.status);
+          __syncwarp();
+          tc_fence_after();
+          const uint64_t a = dQ0 + qs * kStep, b = dK0 + st * kStep;
+          const uint32_t ds = tbase + 128 * s;
+          const bool tile_end = !pair || (i & 1);
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              tc_mma_bf16(tbase + 128 * s, a + (kk >> 2) * 1024 + (kk & 3) * 2, b + (kk >> 2) * 1024 + (kk & 3) * 2,
-                          kIdescS, kk ? 1u : 0u);
+              tc_mma_bf16(ds, a + (kk >> 2) * 1024 + (kk & 3) * 2, b + (kk >> 2) * 1024 + (kk & 3) * 2, kIdescS,
+                          kk ? 1u : 0u);
             tc_commit(&s_full[s]);
-            const bool tile_end = !c.pair || (i & 1);
             if (tile_end) tc_commit(&k_empty[st]);
-            if (i >= ni - 1 - c.pair) tc_commit(&q_empty[qs]);
-            const uint32_t f = (i >= 2 ? 1u : 0u) | (tile_end ? 2u : 0u) | (i >= ni - 2 ? 4u : 0u);
-            if (s) {
-              pv_tile[1] = t;
-              pv_flags[1] = f;
-            } else {
-              pv_tile[0] = t;
-              pv_flags[0] = f;
-            }
+            if (i >= ni - 1 - pair) tc_commit(&q_empty[qs]);
           }
+          __syncwarp();
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          t2 = t1;
+          f2 = f1;
+          t1 = t;
+          f1 = (i >= 2 ? 1u : 0u) | (tile_end ? 2u : 0u) | (i >= ni - 2 ? 4u : 0u);
+          ++cnt;
+          t += tile_end;
         }
-        if (ok) ok = issue_pv(cnt & 1);
-        if (ok) ok = issue_pv((cnt & 1) ^ 1);
-        // every product must be done before TMEM is freed
+      }
+      if (ok && t2 >= 0) ok = __all_sync(0xffffffffu, issue_pv(cnt - 2, t2, f2));
+      if (ok && t1 >= 0) ok = __all_sync(0xffffffffu, issue_pv(cnt - 1, t1, f1));
+      // every product must be done before TMEM is freed
+      if (elect_one()) {
         tc_commit(drain);
         mbar_drain(drain, 0);
       }
@@ -471,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     reg_alloc<kRegsSoftmax>();
     // -------------------------------------------------------- softmax streams
-    const int s = (warp >> 2) - 1;
+    const int s = (warp >> 2) - 1;         // stream
     const int x = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
     const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_addr = tbase + lane_addr + 128 * s;
@@ -479,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int np = 0, ns = 0, no = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status));
+      return __all_sync(0xffffffffu, mbar_sleep(bar, parity, abort_flag, p.status));
     };
     while (ok) {
       const int slot = np % kRing;
@@ -525,67 +585,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int key0 = 128 * (c.j0 + j);
         if (!(ok = wait(&s_full[s], ns & 1))) break;
         ++ns;
-        if (any_valid) {
-          tc_fence_after();
-          float sv[128];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld32(s_addr + 32 * i, *reinterpret_cast<float(*)[32]>(&sv[32 * i]));
-          tc_wait_ld();
-          if (key0 + 128 > vis_min) {
-            const int lim = vis - key0;
-#pragma unroll
-            for (int i = 0; i < 128; ++i) sv[i] = i < lim ? sv[i] : -INFINITY;
-          }
-          float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
-#pragma unroll
-          for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], sv[i]);
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-          if (j < step) {
-            m = top;  // the piece's first tile on this stream: O starts from zero
-          } else if (__any_sync(0xffffffffu, top > m + kRescale)) {
-            // move the reference: S of this tile is ready, so the PV product
-            // before it (same issuing thread) is done and O is still
-            const float mn = fmaxf(m, top);
-            const float f = mn == -INFINITY ? 1.f : ex2_approx(m - mn);
-            l *= f;
-            m = mn;
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-              float ov[32];
-              tmem_ld32(o_addr + 32 * i, ov);
-              tc_wait_ld();
-              uint32_t ou[32];
-#pragma unroll
-              for (int k = 0; k < 32; ++k) ou[k] = __float_as_uint(ov[k] * f);
-              tmem_st32(o_addr + 32 * i, ou);
-            }
-          }
-          const float neg = m == -INFINITY ? 0.f : -m;
-          float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t pk[32];
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const int k = 64 * h + 2 * i;
-              float x0, x1, x2, x3;
-              ffma2(x0, x1, sv[k], sv[k + 1], p.scale_log2, p.scale_log2, neg, neg);
-              ffma2(x2, x3, sv[k + 2], sv[k + 3], p.scale_log2, p.scale_log2, neg, neg);
-              x0 = ex2_approx(x0);
-              x1 = ex2_approx(x1);
-              x2 = ex2_approx(x2);
-              x3 = ex2_approx(x3);
-              fadd2(l0, l1, l0, l1, x0, x1);
-              fadd2(l2, l3, l2, l3, x2, x3);
-              pk[i] = pack_16x2<FP16>(x0, x1);
-              pk[i + 1] = pack_16x2<FP16>(x2, x3);
-            }
-            tmem_st32(s_addr + 32 * h, pk);
-          }
-          l += (l0 + l1) + (l2 + l3);
-          tc_wait_st();
-          tc_fence_before();
-        }
         if (c.len - key0 < 128) {
           // the segment's last tile: clear the V rows past its length
           const int t = c.tiles + j, st = t % kSt;
@@ -598,8 +597,66 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_async_shared();
         }
+        if (any_valid) {
+          tc_fence_after();
+          float sv[128];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32(s_addr + 32 * i, *reinterpret_cast<float(*)[32]>(&sv[32 * i]));
+          tc_wait_ld();
+          if (key0 + 128 > vis_min) {
+            // the masked keys' logits may be anything, NaN included; their
+            // terms come out as 2^-inf = 0
+            const int lim = vis - key0;
+#pragma unroll
+            for (int i = 0; i < 128; ++i) sv[i] = i < lim ? sv[i] : -INFINITY;
+          }
+          float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+          for (int i = 4; i < 124; i += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], sv[i + 2 * k], sv[i + 2 * k + 1]);
+          mx[0] = max3(mx[0], sv[124], sv[125]);
+          mx[1] = max3(mx[1], sv[126], sv[127]);
+          const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * p.scale_log2;
+          if (j < step) {
+            m = top;  // the piece's first tile on this stream: O starts from zero
+          } else if (__any_sync(0xffffffffu, top > m + kRescale)) {
+            // move the reference: S of this tile is ready, so the PV product
+            // before it (same issuing thread) is done and O is still
+            const float mn = fmaxf(m, top);
+            const float f = mn == -INFINITY ? 1.f : ex2_approx(m - mn);
+            l *= f;
+            m = mn;
+#pragma unroll 1
+            for (int i = 0; i < D / 16; ++i) {
+              uint32_t ou[16];
+              tmem_ld16(o_addr + 16 * i, ou);
+              tc_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) ou[k] = __float_as_uint(__uint_as_float(ou[k]) * f);
+              tmem_st16(o_addr + 16 * i, ou);
+            }
+          }
+          const float neg = m == -INFINITY ? 0.f : -m;
+          float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[32];
+            exps<FP16>(sv + 64 * h, p.scale_log2, neg, ls, pk);
+            tmem_st32(s_addr + 32 * h, pk);
+            tc_wait_st();
+            tc_fence_before();
+            if (h == 0) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&p_full[2 * s]);
+            }
+          }
+          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        } else if (lane == 0) {
+          mbar_arrive(&p_full[2 * s]);
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[s]);
+        if (lane == 0) mbar_arrive(&p_full[2 * s + 1]);
       }
       if (!ok) break;
       // the piece's part
@@ -610,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long at =
             (c.prefix ? 0 : p.pre_slots) + (static_cast<long long>(c.slot) * 2 + sub) * stride + x;
         float* po = p.part_o + at * D;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < D / 32; ++i) {
           float ov[32];
           tmem_ld32(o_addr + 32 * i, ov);
@@ -654,7 +711,6 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p, in
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bh = row / p.GT, r = row - bh * p.GT;
   const int b = bh / p.Hkv, hkv = bh - b * p.Hkv;
-  const long long W = p.seg_off[p.nseg];
   float acc[kV];
 #pragma unroll
   for (int i = 0; i < kV; ++i) acc[i] = 0.f;
@@ -664,9 +720,9 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p, in
     // half 0: the prefix, 1: the cache
     if (half == 0 ? p.npre == 0 : p.nseg == p.npre) continue;
     const int seg = half == 0 ? b / p.n : p.npre + b;
-    const long long off = p.seg_off[seg];
+    const long long off = p.seg_off[seg + half], W = p.seg_off[half == 0 ? p.npre : p.nseg + 1];
     const int up = half == 0 ? p.pre_up : p.own_up, rt = half == 0 ? p.pre_rt : p.own_rt;
-    const int nkt = static_cast<int>((p.seg_off[seg + 1] - off) / (p.Hkv * up));
+    const int nkt = static_cast<int>((p.seg_off[seg + half + 1] - off) / (p.Hkv * rt));
     if (nkt == 0) continue;
     int tile, x, stride;
     if (half == 0) {
@@ -686,7 +742,9 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p, in
     }
     const int lu = hkv * up + (tile >> 1);
     const bool pair = (tile | 1) < rt;
-    const long long o0 = off + static_cast<long long>(lu) * nkt, o1 = o0 + nkt;
+    const int w = pair ? 2 : 1;
+    const long long o0 = off + (static_cast<long long>(hkv) * rt + (tile & ~1)) * nkt;
+    const long long o1 = o0 + static_cast<long long>(w) * nkt;
     const int c0 = static_cast<int>(((o0 + 1) * grid - 1) / W), c1 = static_cast<int>((o1 * grid - 1) / W);
     const long long unit = static_cast<long long>(half == 0 ? seg : b) * p.Hkv * up + lu;
     const long long base = half == 0 ? 0 : p.pre_slots;
@@ -694,7 +752,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p, in
     for (int q = (warp - turn) & 3; q < (c1 - c0 + 1) * nsub; q += 4) {
       const int c = c0 + (pair ? q : q >> 1);
       const int sub = pair ? (tile & 1) : (q & 1);
-      const long long lo = max(o0, W * c / grid), hi = min(o1, W * (c + 1) / grid);
+      const long long lo = tiles_before(max(o0, W * c / grid), o0, w);
+      const long long hi = tiles_before(min(o1, W * (c + 1) / grid), o0, w);
       if (hi <= lo || (!pair && sub >= hi - lo)) continue;
       const long long at = base + ((unit + c) * 2 + sub) * stride + x;
       const float2 ml = p.part_ml[at];
@@ -788,7 +847,7 @@ bool make_plan(Plan& w, int B, int G, int Hkv, int T, int d, int Bp, int P, int 
   w.part_rows = p.pre_slots + (C > 0 ? (w.own_units + kMaxCtas) * 2 * p.own_rb : 0);
   size_t o = 256;
   w.off_seg = o;
-  o += align256(static_cast<size_t>(p.nseg + 1) * 8);
+  o += align256(static_cast<size_t>(p.nseg + 2) * 8);
   w.off_ml = o;
   o += align256(static_cast<size_t>(w.part_rows) * 8);
   w.off_o = o;
@@ -848,7 +907,7 @@ cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t st) {
   if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
   if (a.P == 0) m[2] = m[4], m[3] = m[5];
   if (a.C == 0) m[4] = m[2], m[5] = m[3];
-  // one CTA per SM; no more than there can be tiles
+  // one CTA per SM; no more than there can be tiles (a pair's count once)
   const long long tiles = w.pre_units * ((a.P + 127LL) / 128) + w.own_units * ((a.C + 127LL) / 128);
   int grid = device_sm_count();
   if (grid > kMaxCtas) grid = kMaxCtas;

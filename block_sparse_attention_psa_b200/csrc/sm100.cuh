@@ -86,6 +86,32 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
   }
 }
 
+// The same wait with the warp asleep between looks: the barrier wakes it, or a
+// time limit of 50 us after which the abort flag and the budget are checked.
+__device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  const uint32_t addr = smem_u32(bar);
+  long long t0 = 0;
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(addr), "r"(parity), "r"(50000u)
+        : "memory");
+    if (ok) return true;
+    if (*abort_flag) return false;
+    if (t0 == 0) {
+      t0 = clock64();
+    } else if (clock64() - t0 > kWaitCycles) {
+      *abort_flag = 1;
+      record_status(status, kStatusTimeout);
+      return false;
+    }
+  }
+}
+
 // ---------------------------------------------------------------- proxies
 __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -236,6 +262,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&u)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
+        "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 // The mirror of tmem_ld32: 32 registers of this thread to its lane, columns
 // [col, col + 32).
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&u)[32]) {
@@ -249,7 +285,25 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&u)[32
         "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&u)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]),
+        "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
+      : "memory");
+}
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// One lane of a converged warp (true in exactly one).  A branch on it keeps
+// the warp's control flow uniform for the compiler, so that the operands of
+// a tcgen05.mma inside it stay in uniform registers; a branch on a lane
+// number does not, and costs an extra move per operand and product.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p != 0;
+}
 
 // ---------------------------------------------------------------- descriptors
 // Shared-memory matrix descriptor (tcgen05 format): start address, leading
@@ -316,6 +370,64 @@ __device__ __forceinline__ void fadd2(float& d0, float& d1, float a0, float a1, 
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
+
+__device__ __forceinline__ void fmul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// A pair of exponentials on the FMA pipe: 2^x = p * s with s = 2^n, n the
+// integer nearest x, and p the minimax polynomial of 2^f on [-1/2, 1/2]
+// (coefficients by a Remez exchange for the relative error: 2.6e-6 at degree
+// 4, 7.5e-8 at degree 5).  n is read off the low bits of x + 1.5 * 2^23 +
+// 127, which are also the exponent field of s.  x below -126 counts as -126,
+// x from 128 on gives infinity, NaN gives NaN.
+template <int DEG>
+__device__ __forceinline__ void exp2_parts(float x0, float x1, float& p0, float& p1, float& s0, float& s1) {
+  static_assert(DEG == 4 || DEG == 5, "");
+  constexpr float kBias = 12583039.0f;
+  x0 = min_nan(max_nan(x0, -126.0f), 128.0f);
+  x1 = min_nan(max_nan(x1, -126.0f), 128.0f);
+  float t0, t1, f0, f1;
+  fadd2(t0, t1, x0, x1, kBias, kBias);
+  ffma2(f0, f1, t0, t1, -1.0f, -1.0f, kBias, kBias);
+  fadd2(f0, f1, f0, f1, x0, x1);
+  if constexpr (DEG == 5) {
+    ffma2(p0, p1, f0, f1, 0.0013276472f, 0.0013276472f, 0.00967554133f, 0.00967554133f);
+    ffma2(p0, p1, p0, p1, f0, f1, 0.0555071327f, 0.0555071327f);
+    ffma2(p0, p1, p0, p1, f0, f1, 0.240221197f, 0.240221197f);
+    ffma2(p0, p1, p0, p1, f0, f1, 0.693146967f, 0.693146967f);
+    ffma2(p0, p1, p0, p1, f0, f1, 1.00000007f, 1.00000007f);
+  } else {
+    ffma2(p0, p1, f0, f1, 0.00957010191f, 0.00957010191f, 0.0559178603f, 0.0559178603f);
+    ffma2(p0, p1, p0, p1, f0, f1, 0.240247448f, 0.240247448f);
+    ffma2(p0, p1, p0, p1, f0, f1, 0.693121815f, 0.693121815f);
+    ffma2(p0, p1, p0, p1, f0, f1, 0.999999261f, 0.999999261f);
+  }
+  s0 = __uint_as_float(__float_as_uint(t0) << 23);
+  s1 = __uint_as_float(__float_as_uint(t1) << 23);
+}
+
+// Largest of three (one instruction on sm_100).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;

@@ -14,17 +14,28 @@
 //    operations and one exponential per (query, key) pair: an SM's tensor
 //    core takes 256 cycles for a tile, its 16 exponentials a cycle 1024, so
 //    it is bound by the exponentials.
-//  * Unit: a pair of key tiles (256 keys) of one KV head, held in shared
-//    memory, with the query tiles streamed past it; each of the two
-//    warpgroups owns one key tile, so a query tile is loaded once for both,
-//    and each has two S buffers (512 TMEM columns in all).
+//  * Up to 32 queries per key (decode): stream_kernel. 16 keys x 8 queries per
+//    mma.sync, with K going from DRAM straight to registers: a thread's four
+//    16-byte pieces of two key rows are its A operands, in an order of the d
+//    features that the queries' registers share. No shared memory and no barriers, so nothing
+//    stands between the loads; the legacy tensor path has an order of
+//    magnitude to spare at this ratio.
+//  * More: weight_kernel. Unit: a pair of key tiles (256 keys) of one KV head,
+//    held in shared memory, with the query tiles streamed past it; each of the
+//    two warpgroups owns one key tile, so a query tile is loaded once for
+//    both, and each has two S buffers (512 TMEM columns in all). One warp
+//    works out the units and publishes them; the others only step through
+//    them (divisions in every role had cost more than the products).
 //  * Query tiles: T >= 128 tokens: 128 tokens of one head, so that causal
 //    tiles past the diagonal are skipped; fewer: up to 128 of the G T rows
 //    that share the KV head, over several sequences when they share the keys.
-//  * Units go to the CTAs in turn, forwards and backwards, heaviest (fewest
-//    keys hidden) first.  When there are fewer units than two per SM the query
-//    tiles of a unit are split over several, whose sums a second kernel adds
-//    in a fixed order.
+//  * Units of equal cost (T < 128) lie on one line that is cut into equal
+//    runs; a prefill's go to the CTAs in turn, forwards and backwards, heaviest
+//    (fewest keys hidden) first.  When there are fewer units than two per SM the
+//    query tiles of a unit are split over several, whose sums a second kernel
+//    adds in a fixed order.
+//  * A quarter of the exponentials runs on the FMA pipe (exp2_parts, 7.5e-8),
+//    whose other work leaves it half idle.
 //  * Sums: 128 columns in four fp32 accumulators, tile sums added with a
 //    compensation term (a key of a long prefill sums 10^5 terms).
 // Every wait is bounded.
@@ -36,11 +47,13 @@
 namespace psa {
 namespace {
 
-constexpr int kThreads = 384;      // WG0: K/Q loads, MMA issue, lse loads; WG1, WG2: one key tile each
+constexpr int kThreads = 384;      // WG0: K/Q loads, MMA issue, lse loads, units; WG1, WG2: one key tile each
 constexpr int kRegsProducer = 72;  // 128 x 72 + 256 x 216 = 384 x 168
 constexpr int kRegsSum = 216;
 constexpr int kLse = 4;            // query tiles whose lse is in shared memory
+constexpr int kRing = 4;           // units in flight
 constexpr int kPlanSms = 148;      // SMs the split is planned for (fixed: it sizes the workspace)
+constexpr int kPoly = 2;           // of eight pairs of exponentials, those on the FMA pipe
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
@@ -52,7 +65,7 @@ struct Cfg {
   static constexpr int kOffQ = 4 * kTile;
   static constexpr int kOffLse = kOffQ + kQStages * kTile;
   static constexpr int kOffMisc = kOffLse + kLse * 1024;
-  static constexpr int kSmem = kOffMisc + 512 + 1024;  // + alignment slack
+  static constexpr int kSmem = kOffMisc + 1024 + 1024;  // + alignment slack
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
 
@@ -66,16 +79,21 @@ struct Params {
   int GT, by_head;        // by_head: query tiles of one head
   int nb, rb;             // query tile: sequences x rows (box)
   int tiles;              // by_head: tiles of one head; else row tiles of a KV head (all n sequences)
-  int Z, pairs, units;
+  int Z, pairs;
+  long long units;
   float scale_log2;
   int* status;
 };
 
+// A unit, as the scheduler publishes it.
 struct Unit {
   int bk, hkv, key0, len;
-  int t_min, per;         // by_head: first visible tile, tiles per head
-  int f0, f1;             // query tiles of this unit
+  int nt;          // query tiles; -1 ends the walk
+  int i, g, r0;    // first tile: sequence of the group, query head of the KV head (by_head), row
+  int r_min;       // by_head: first visible row of every head
+  int z;
 };
+constexpr int kUnitInts = sizeof(Unit) / 4;
 
 __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
   const long long t0 = clock64();
@@ -97,64 +115,94 @@ __device__ __forceinline__ int clamped_len(const Params& p, int bk) {
   return min(max(n, 0), p.C);
 }
 
-// The w-th unit of this CTA, or -1: rows of gridDim.x units, every other row
-// taken backwards.
-__device__ __forceinline__ int unit_id(const Params& p, int w) {
-  const int g = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
-  const long long u = static_cast<long long>(w) * g + ((w & 1) ? g - 1 - c : c);
-  return u < p.units ? static_cast<int>(u) : (static_cast<long long>(w) * g < p.units ? -2 : -1);
-}
+// Query tile of a unit; next() steps to the following one.
+struct Tile {
+  int i, g, r0;
+  __device__ __forceinline__ void next(const Params& p, const Unit& x) {
+    if (p.by_head) {
+      r0 += 128;
+      if (r0 >= p.T) {
+        r0 = x.r_min;
+        if (++g == p.G) {
+          g = 0;
+          ++i;
+        }
+      }
+    } else if (p.GT >= 128) {
+      r0 += 128;
+      if (r0 >= p.GT) {
+        r0 = 0;
+        ++i;
+      }
+    } else {
+      i += p.nb;
+    }
+  }
+  // valid columns
+  __device__ __forceinline__ int cols(const Params& p) const {
+    if (p.by_head) return min(128, p.T - r0);
+    if (p.GT >= 128) return min(128, p.GT - r0);
+    return min(p.nb, p.n - i) * p.GT;
+  }
+};
 
-__device__ __forceinline__ int unit_bk(const Params& p, int u) { return u % (p.Bk * p.Hkv) / p.Hkv; }
-
-__device__ __forceinline__ Unit make_unit(const Params& p, int u, int len) {
+// Unit (row of heads bh, key pair, part z) with its tiles.
+__device__ __forceinline__ Unit make_unit(const Params& p, int bh, int pair, int z, int len) {
   Unit x;
-  const int bh = u % (p.Bk * p.Hkv), pz = u / (p.Bk * p.Hkv);
-  const int pair = pz / p.Z, z = pz - pair * p.Z;
   x.bk = bh / p.Hkv;
   x.hkv = bh - x.bk * p.Hkv;
   x.key0 = 256 * pair;
   x.len = len;
-  int total = p.tiles;
-  x.t_min = 0;
-  x.per = p.tiles;
+  x.z = z;
+  x.r_min = 0;
+  int per = p.tiles, total = p.tiles;
   if (p.by_head) {
     // token t sees key j iff j <= len - T + t
-    if (p.causal) x.t_min = max(0, x.key0 - (len - p.T)) / 128;
-    x.per = max(p.tiles - x.t_min, 0);
-    total = p.n * p.G * x.per;
+    const int t_min = p.causal ? max(0, x.key0 - (len - p.T)) / 128 : 0;
+    x.r_min = 128 * t_min;
+    per = max(p.tiles - t_min, 0);
+    total = p.n * p.G * per;
   }
   if (x.key0 >= len) total = 0;
-  x.f0 = static_cast<int>(static_cast<long long>(total) * z / p.Z);
-  x.f1 = static_cast<int>(static_cast<long long>(total) * (z + 1) / p.Z);
+  const int f0 = static_cast<int>(static_cast<long long>(total) * z / p.Z);
+  const int f1 = static_cast<int>(static_cast<long long>(total) * (z + 1) / p.Z);
+  x.nt = f1 - f0;
+  x.i = x.g = x.r0 = 0;
+  if (x.nt > 0) {
+    if (p.by_head) {
+      const int o = f0 / per;
+      x.i = o / p.G;
+      x.g = o - x.i * p.G;
+      x.r0 = x.r_min + 128 * (f0 - o * per);
+    } else if (p.GT >= 128) {
+      const int of = (p.GT + 127) / 128;
+      x.i = f0 / of;
+      x.r0 = 128 * (f0 - x.i * of);
+    } else {
+      x.i = f0 * p.nb;
+    }
+  }
   return x;
 }
 
-// Query tile f of a unit.
-struct Tile {
-  int b, head, r0;  // first sequence, query head (by_head) and row
-  int cols;         // valid columns
-};
-__device__ __forceinline__ Tile make_tile(const Params& p, const Unit& x, int f) {
-  Tile t;
-  t.head = 0;
-  if (p.by_head) {
-    const int o = f / x.per, i = o / p.G;
-    t.b = x.bk * p.n + i;
-    t.head = x.hkv * p.G + (o - i * p.G);
-    t.r0 = 128 * (x.t_min + f - o * x.per);
-    t.cols = min(128, p.T - t.r0);
-  } else if (p.GT >= 128) {
-    const int per = (p.GT + 127) / 128, i = f / per;
-    t.b = x.bk * p.n + i;
-    t.r0 = 128 * (f - i * per);
-    t.cols = min(128, p.GT - t.r0);
-  } else {
-    t.b = x.bk * p.n + f * p.nb;
-    t.r0 = 0;
-    t.cols = min(p.nb, p.n - f * p.nb) * p.GT;
+// Sum of 2^(v * scale + nl) over 32 columns; nl from shared memory.
+__device__ __forceinline__ void sum32(const float (&v)[32], const float* nl, float scale, float (&a)[4]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    const float4 l4 = *reinterpret_cast<const float4*>(nl + i);
+    float x0, x1, x2, x3;
+    ffma2(x0, x1, v[i], v[i + 1], scale, scale, l4.x, l4.y);
+    ffma2(x2, x3, v[i + 2], v[i + 3], scale, scale, l4.z, l4.w);
+    fadd2(a[0], a[1], a[0], a[1], ex2_approx(x0), ex2_approx(x1));
+    const int k = (i / 4) % 4;
+    if (k < kPoly) {
+      float p0, p1, s0, s1;
+      exp2_parts<5>(x2, x3, p0, p1, s0, s1);
+      ffma2(a[2], a[3], p0, p1, s0, s1, a[2], a[3]);
+    } else {
+      fadd2(a[2], a[3], a[2], a[3], ex2_approx(x2), ex2_approx(x3));
+    }
   }
-  return t;
 }
 
 template <int D, bool FP16>
@@ -177,9 +225,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* s_empty = bars + 16;  // [2 streams][2] read             (4 warps)
   uint64_t* l_full = bars + 20;   // [kLse] lse of a query tile      (lse warp)
   uint64_t* l_empty = bars + 24;  // [kLse] read                     (8 warps)
-  uint64_t* drain = bars + 28;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc + 256);
+  uint64_t* u_full = bars + 28;   // [kRing] a unit published
+  uint64_t* u_empty = bars + 32;  // [kRing] read by loads, MMA issue, lse loads, 8 warps
+  uint64_t* drain = bars + 36;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc + 320);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* start_bk = reinterpret_cast<int*>(tmem_slot + 2);
+  long long* start_off = reinterpret_cast<long long*>(smem + C::kOffMisc + 336);
+  long long* red = start_off + 1;                                                  // [12]
+  volatile int* ring = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 512);  // [kRing][kUnitInts]
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
@@ -198,6 +252,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kLse; ++i) {
       mbar_init(&l_full[i], 1);
       mbar_init(&l_empty[i], 8);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&u_full[i], 1);
+      mbar_init(&u_empty[i], 11);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -229,154 +287,276 @@ __global__ void __launch_bounds__(kThreads, 1)
     bad = __syncthreads_or(bad);
     if (threadIdx.x == 0) *p.status = bad ? kStatusLength : 0;
   }
-
-  // Every role walks the CTA's units on its own, with the next unit's length
-  // loaded ahead.  unit_id: -1 ends the walk, -2 is an empty place of the last row.
-  auto first = [&](int& u, int& len) {
-    u = unit_id(p, 0);
-    len = u >= 0 ? clamped_len(p, unit_bk(p, u)) : 0;
-  };
+  // Units of equal cost: the line of all valid (key set, head, pair, part),
+  // and where this CTA's run of it starts.
+  long long x0 = 0, x1 = 0;
+  if (!p.by_head) {
+    const int per = p.Hkv * p.Z;
+    long long mine = 0;
+    for (int i = threadIdx.x; i < p.Bk; i += kThreads)
+      mine += static_cast<long long>((clamped_len(p, i) + 255) / 256) * per;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) red[warp] = mine;
+    __syncthreads();
+    long long total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) total += red[w];
+    x0 = total * blockIdx.x / gridDim.x;
+    x1 = total * (blockIdx.x + 1) / gridDim.x;
+    long long run = 0;
+    for (int b0 = 0; b0 < p.Bk && x0 < x1; b0 += kThreads) {
+      const int bk = b0 + threadIdx.x;
+      const long long t = bk < p.Bk ? static_cast<long long>((clamped_len(p, bk) + 255) / 256) * per : 0;
+      long long inc = t;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+      }
+      __syncthreads();
+      if (lane == 31) red[warp] = inc;
+      __syncthreads();
+      long long base = run;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        base += w < warp ? red[w] : 0;
+        run += red[w];
+      }
+      if (base + inc - t <= x0 && x0 < base + inc) {
+        *start_bk = bk;
+        *start_off = base + inc - t;
+      }
+    }
+    __syncthreads();
+  }
 
   if (warp < 4) {
     reg_dealloc<kRegsProducer>();
-    if (warp == 0 && lane == 0) {
+    int nu = 0;
+    // the next unit for a single thread or a whole warp; nt < 0 at the end or on a timeout
+    auto next_unit = [&](Unit& x, bool reads) {
+      const int slot = nu % kRing;
+      if (!mbar_sleep(&u_full[slot], (nu / kRing) & 1, abort_flag, p.status)) {
+        x.nt = -1;
+        return;
+      }
+      int* w = reinterpret_cast<int*>(&x);
+#pragma unroll
+      for (int i = 0; i < kUnitInts; ++i) w[i] = ring[slot * kUnitInts + i];
+      if (reads) mbar_arrive(&u_empty[slot]);
+      ++nu;
+    };
+    if (warp == 3) {
+      // ---------------------------------------------------- units
+      if (lane == 0) {
+        bool ok = true;
+        auto publish = [&](const Unit& x) -> bool {
+          const int slot = nu % kRing;
+          if (nu >= kRing && !mbar_sleep(&u_empty[slot], ((nu / kRing) - 1) & 1, abort_flag, p.status)) return false;
+          const int* w = reinterpret_cast<const int*>(&x);
+          for (int i = 0; i < kUnitInts; ++i) ring[slot * kUnitInts + i] = w[i];
+          mbar_arrive(&u_full[slot]);
+          ++nu;
+          return true;
+        };
+        if (p.by_head) {
+          const int BH = p.Bk * p.Hkv, g = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
+          for (long long w = 0; ok && w * g < p.units; ++w) {
+            const long long u = w * g + ((w & 1) ? g - 1 - c : c);
+            if (u >= p.units) continue;
+            const long long pz = u / BH;
+            const int bh = static_cast<int>(u - pz * BH), pair = static_cast<int>(pz / p.Z);
+            ok = publish(make_unit(p, bh, pair, static_cast<int>(pz - static_cast<long long>(pair) * p.Z),
+                                   clamped_len(p, bh / p.Hkv)));
+          }
+        } else if (x0 < x1) {
+          int bk = *start_bk;
+          int len = clamped_len(p, bk), pairs = (len + 255) / 256;
+          long long rel = x0 - *start_off;  // place inside the key set: (head, pair, part)
+          int hkv = static_cast<int>(rel / (static_cast<long long>(pairs) * p.Z));
+          rel -= static_cast<long long>(hkv) * pairs * p.Z;
+          int pair = static_cast<int>(rel / p.Z), z = static_cast<int>(rel - static_cast<long long>(pair) * p.Z);
+          for (long long x = x0; ok && x < x1; ++x) {
+            ok = publish(make_unit(p, bk * p.Hkv + hkv, pair, z, len));
+            if (++z < p.Z) continue;
+            z = 0;
+            if (++pair < pairs) continue;
+            pair = 0;
+            if (++hkv < p.Hkv || x + 1 >= x1) continue;
+            hkv = 0;
+            do {  // the run goes on, so a key set with keys follows
+              ++bk;
+              len = clamped_len(p, bk);
+            } while (len == 0);
+            pairs = (len + 255) / 256;
+          }
+        }
+        Unit end = {};
+        end.nt = -1;
+        if (ok) publish(end);
+      }
+    } else if (warp == 0 && lane == 0) {
       // ---------------------------------------------------- K and Q loads
       int ku = 0, qt = 0;  // pairs and query tiles loaded
       bool ok = true;
-      int u, len;
-      first(u, len);
-      for (int w = 0; ok && u != -1; ++w) {
-        const int un = unit_id(p, w + 1), ln = un >= 0 ? clamped_len(p, unit_bk(p, un)) : 0;
-        if (u >= 0) {
-          const Unit x = make_unit(p, u, len);
-          if (x.f0 < x.f1) {
-            const int kb = ku & 1;
-            ok = mbar_wait(&k_empty[kb], ((ku >> 1) & 1) ^ 1, abort_flag, p.status);
-            if (!ok) break;
-            // 64-key boxes; none that starts past the length
-            const int boxes = min(4, (x.len - x.key0 + 63) / 64);
-            mbar_arrive_expect_tx(&k_full[kb], boxes * 64 * 128 * C::kChunks);
-            for (int i = 0; i < boxes; ++i)
+      for (;;) {
+        Unit x;
+        next_unit(x, true);
+        if (x.nt < 0 || !ok) break;
+        if (x.nt == 0) continue;
+        const int kb = ku & 1;
+        if (!(ok = mbar_sleep(&k_empty[kb], ((ku >> 1) & 1) ^ 1, abort_flag, p.status))) break;
+        // 64-key boxes; none that starts past the length
+        const int boxes = min(4, (x.len - x.key0 + 63) / 64);
+        mbar_arrive_expect_tx(&k_full[kb], boxes * 64 * 128 * C::kChunks);
+        for (int i = 0; i < boxes; ++i)
 #pragma unroll
-              for (int ch = 0; ch < C::kChunks; ++ch)
-                tma_load_3d(&tmK, sK + (2 * kb + (i >> 1)) * C::kTile + ch * 16384 + (i & 1) * 8192, &k_full[kb],
-                            64 * ch, x.key0 + 64 * i, x.bk * p.Hkv + x.hkv);
-            ++ku;
-            for (int f = x.f0; f < x.f1; ++f, ++qt) {
-              const int st = qt % kQ;
-              ok = mbar_wait(&q_empty[st], ((qt / kQ) & 1) ^ 1, abort_flag, p.status);
-              if (!ok) break;
-              const Tile t = make_tile(p, x, f);
-              mbar_arrive_expect_tx(&q_full[st], static_cast<uint32_t>(p.nb * p.rb) * 128 * C::kChunks);
+          for (int ch = 0; ch < C::kChunks; ++ch)
+            tma_load_3d(&tmK, sK + (2 * kb + (i >> 1)) * C::kTile + ch * 16384 + (i & 1) * 8192, &k_full[kb],
+                        64 * ch, x.key0 + 64 * i, x.bk * p.Hkv + x.hkv);
+        ++ku;
+        Tile t = {x.i, x.g, x.r0};
+        const uint32_t bytes = static_cast<uint32_t>(p.nb * p.rb) * 128 * C::kChunks;
+        for (int f = 0; f < x.nt; ++f, ++qt) {
+          const int st = qt % kQ;
+          if (!(ok = mbar_sleep(&q_empty[st], ((qt / kQ) & 1) ^ 1, abort_flag, p.status))) break;
+          mbar_arrive_expect_tx(&q_full[st], bytes);
 #pragma unroll
-              for (int ch = 0; ch < C::kChunks; ++ch)
-                tma_load_4d(&tmQ, sQ + st * C::kTile + ch * 16384, &q_full[st], 64 * ch, t.r0,
-                            p.by_head ? t.head : x.hkv, t.b);
-            }
-          }
+          for (int ch = 0; ch < C::kChunks; ++ch)
+            tma_load_4d(&tmQ, sQ + st * C::kTile + ch * 16384, &q_full[st], 64 * ch, t.r0,
+                        p.by_head ? x.hkv * p.G + t.g : x.hkv, x.bk * p.n + t.i);
+          t.next(p, x);
         }
-        u = un;
-        len = ln;
       }
       // no bulk copy may still be writing shared memory when the CTA leaves
       for (int i = max(0, ku - 2); i < ku; ++i) mbar_drain(&k_full[i & 1], (i >> 1) & 1);
       for (int i = max(0, qt - kQ); i < qt; ++i) mbar_drain(&q_full[i % kQ], (i / kQ) & 1);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
       // ---------------------------------------------------- MMA issue
+      // The whole warp walks the tiles in step; one elected lane issues.  The
+      // lanes wait without a vote and agree on stopping once per tile.
       const uint64_t dK0 = sdesc_sw128(smem_u32(sK), 16, 1024);
       const uint64_t dQ0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
       constexpr uint64_t kStep = C::kTile >> 4;
       int ku = 0, qt = 0;
       bool ok = true;
-      int u, len;
-      first(u, len);
-      for (int w = 0; ok && u != -1; ++w) {
-        const int un = unit_id(p, w + 1), ln = un >= 0 ? clamped_len(p, unit_bk(p, un)) : 0;
-        if (u >= 0) {
-          const Unit x = make_unit(p, u, len);
-          if (x.f0 < x.f1) {
-            const int kb = ku & 1;
-            if (!(ok = mbar_wait(&k_full[kb], (ku >> 1) & 1, abort_flag, p.status))) break;
-            for (int f = x.f0; f < x.f1 && ok; ++f, ++qt) {
-              const int st = qt % kQ, buf = qt & 1;
-              const Tile t = make_tile(p, x, f);
-              const uint32_t idesc = idesc_f16_f32(FP16, 128, (t.cols + 15) & ~15, 0, 0);
-              if (!(ok = mbar_wait(&q_full[st], (qt / kQ) & 1, abort_flag, p.status))) break;
+      while (ok) {
+        Unit x;
+        next_unit(x, false);
+        __syncwarp();
+        const int nt = __shfl_sync(0xffffffffu, x.nt, 0);
+        if (nt < 0) break;
+        if (elect_one()) mbar_arrive(&u_empty[(nu - 1) % kRing]);
+        if (nt == 0) continue;
+        const int kb = ku & 1;
+        ok = mbar_sleep(&k_full[kb], (ku >> 1) & 1, abort_flag, p.status);
+        Tile t = {x.i, x.g, x.r0};
+        for (int f = 0; f < nt; ++f, ++qt) {
+          const int st = qt % kQ, buf = qt & 1;
+          const uint32_t idesc =
+              idesc_f16_f32(FP16, 128, __shfl_sync(0xffffffffu, (t.cols(p) + 15) & ~15, 0), 0, 0);
+          const uint32_t eh = ((qt >> 1) & 1) ^ 1, qh = (qt / kQ) & 1;
+          const bool r0 = mbar_try_wait(&s_empty[buf], eh), rq = mbar_try_wait(&q_full[st], qh);
+          if (!rq) ok &= mbar_sleep(&q_full[st], qh, abort_flag, p.status);
+          if (!r0) ok &= mbar_sleep(&s_empty[buf], eh, abort_flag, p.status);
+          const uint64_t a = dK0 + 2 * kb * kStep, b = dQ0 + st * kStep;
+          __syncwarp();
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-              for (int s = 0; s < 2; ++s) {
-                if (!(ok = mbar_wait(&s_empty[2 * s + buf], ((qt >> 1) & 1) ^ 1, abort_flag, p.status))) break;
-                tc_fence_after();
-                const uint64_t a = dK0 + (2 * kb + s) * kStep, b = dQ0 + st * kStep;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                  tc_mma_bf16(tbase + 256 * s + 128 * buf, a + (kk >> 2) * 1024 + (kk & 3) * 2,
-                              b + (kk >> 2) * 1024 + (kk & 3) * 2, idesc, kk ? 1u : 0u);
-                tc_commit(&s_full[2 * s + buf]);
-              }
-              if (!ok) break;
-              tc_commit(&q_empty[st]);
-              if (f == x.f1 - 1) tc_commit(&k_empty[kb]);
-            }
-            ++ku;
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc_mma_bf16(tbase + 128 * buf, a + (kk >> 2) * 1024 + (kk & 3) * 2,
+                          b + (kk >> 2) * 1024 + (kk & 3) * 2, idesc, kk ? 1u : 0u);
+            tc_commit(&s_full[buf]);
           }
+          __syncwarp();
+          ok &= mbar_sleep(&s_empty[2 + buf], eh, abort_flag, p.status);
+          __syncwarp();
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc_mma_bf16(tbase + 256 + 128 * buf, a + kStep + (kk >> 2) * 1024 + (kk & 3) * 2,
+                          b + (kk >> 2) * 1024 + (kk & 3) * 2, idesc, kk ? 1u : 0u);
+            tc_commit(&s_full[2 + buf]);
+            tc_commit(&q_empty[st]);
+            if (f == nt - 1) tc_commit(&k_empty[kb]);
+          }
+          __syncwarp();
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          t.next(p, x);
         }
-        u = un;
-        len = ln;
+        ++ku;
       }
-      tc_commit(drain);
-      mbar_drain(drain, 0);
+      if (elect_one()) {
+        tc_commit(drain);
+        mbar_drain(drain, 0);
+      }
     } else if (warp == 2) {
       // ---------------------------------------------------- lse and limits per column
       int qt = 0;
       bool ok = true;
-      int u, len;
-      first(u, len);
-      for (int w = 0; ok && u != -1; ++w) {
-        const int un = unit_id(p, w + 1), ln = un >= 0 ? clamped_len(p, unit_bk(p, un)) : 0;
-        if (u >= 0) {
-          const Unit x = make_unit(p, u, len);
-          for (int f = x.f0; f < x.f1; ++f, ++qt) {
-            const Tile t = make_tile(p, x, f);
-            float v[4];
-            int lim[4];
+      while (ok) {
+        Unit x;
+        next_unit(x, false);
+        __syncwarp();
+        if (__any_sync(0xffffffffu, x.nt < 0)) break;
+        if (lane == 0) mbar_arrive(&u_empty[(nu - 1) % kRing]);
+        Tile t = {x.i, x.g, x.r0};
+        // this lane's values of a tile
+        float v[4];
+        int lim[4];
+        auto load = [&](const Tile& t) {
+          const int cols = t.cols(p);
+          const int b = x.bk * p.n + t.i;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int c = lane + 32 * i;
-              v[i] = INFINITY;
-              lim[i] = -1;
-              if (c < t.cols) {
-                long long at;
-                int tok;
-                if (p.by_head) {
-                  tok = t.r0 + c;
-                  at = (static_cast<long long>(t.b) * p.Hkv * p.G + t.head) * p.T + tok;
-                } else if (p.GT >= 128) {
-                  tok = (t.r0 + c) % p.T;
-                  at = (static_cast<long long>(t.b) * p.Hkv + x.hkv) * p.GT + t.r0 + c;
-                } else {
-                  const int i2 = c / p.GT, r = c - i2 * p.GT;
-                  tok = r % p.T;
-                  at = (static_cast<long long>(t.b + i2) * p.Hkv + x.hkv) * p.GT + r;
-                }
-                const float l = __ldg(p.lse + at);
-                v[i] = l == -INFINITY ? INFINITY : l * kLog2e;  // a query that saw nothing adds nothing
-                lim[i] = p.causal ? x.len - p.T + tok : INT_MAX;
+          for (int i = 0; i < 4; ++i) {
+            const int c = lane + 32 * i;
+            v[i] = -INFINITY;
+            lim[i] = -1;
+            if (c < cols) {
+              long long at;
+              int tok;
+              if (p.by_head) {
+                tok = t.r0 + c;
+                at = (static_cast<long long>(b) * p.Hkv * p.G + x.hkv * p.G + t.g) * p.T + tok;
+              } else if (p.GT >= 128) {
+                tok = (t.r0 + c) % p.T;
+                at = (static_cast<long long>(b) * p.Hkv + x.hkv) * p.GT + t.r0 + c;
+              } else {
+                const int i2 = c / p.GT, r = c - i2 * p.GT;
+                tok = r % p.T;
+                at = (static_cast<long long>(b + i2) * p.Hkv + x.hkv) * p.GT + r;
               }
+              v[i] = __ldg(p.lse + at);
+              lim[i] = p.causal ? x.len - p.T + tok : INT_MAX;
             }
-            const int st = qt % kLse;
-            ok = __all_sync(0xffffffffu, mbar_wait(&l_empty[st], ((qt / kLse) & 1) ^ 1, abort_flag, p.status));
-            if (!ok) break;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              sLse[128 * st + lane + 32 * i] = v[i];
-              sLim[128 * st + lane + 32 * i] = lim[i];
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&l_full[st]);
           }
+        };
+        if (x.nt > 0) load(t);
+        for (int f = 0; f < x.nt; ++f, ++qt) {
+          float nl[4];
+          int lm[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // a query that saw nothing (lse -inf) adds nothing
+            nl[i] = v[i] == -INFINITY ? -INFINITY : -v[i] * kLog2e;
+            lm[i] = lim[i];
+          }
+          if (f + 1 < x.nt) {
+            t.next(p, x);
+            load(t);  // on its way while this one is handed over
+          }
+          const int st = qt % kLse;
+          ok = __all_sync(0xffffffffu, mbar_sleep(&l_empty[st], ((qt / kLse) & 1) ^ 1, abort_flag, p.status));
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            sLse[128 * st + lane + 32 * i] = nl[i];
+            sLim[128 * st + lane + 32 * i] = lm[i];
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&l_full[st]);
         }
-        u = un;
-        len = ln;
       }
     }
     __syncwarp();
@@ -386,56 +566,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int s = (warp >> 2) - 1;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t s_addr = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256 * s;
-    int qt = 0;
+    int nu = 0, qt = 0;
     bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status));
-    };
-    int u, len;
-    first(u, len);
-    for (int w = 0; ok && u != -1; ++w) {
-      const int un = unit_id(p, w + 1), ln = un >= 0 ? clamped_len(p, unit_bk(p, un)) : 0;
-      if (u >= 0) {
-        const Unit x = make_unit(p, u, len);
-        const int tile0 = x.key0 + 128 * s, key = tile0 + row;
-        const long long at = static_cast<long long>(x.bk * p.Hkv + x.hkv) * p.C + key;
-        const float before = p.Z == 1 && p.score_in && key < x.len ? p.score_in[at] : 0.f;
-        float acc = 0.f, comp = 0.f;
-        for (int f = x.f0; f < x.f1; ++f, ++qt) {
-          const int buf = qt & 1, st = qt % kLse;
-          const Tile t = make_tile(p, x, f);
-          const bool mask =
-              p.causal && tile0 + 127 > x.len - p.T + (p.by_head ? t.r0 : 0);
-          if (!(ok = wait(&l_full[st], (qt / kLse) & 1))) break;
-          if (!(ok = wait(&s_full[2 * s + buf], (qt >> 1) & 1))) break;
-          tc_fence_after();
-          const float* ls = sLse + 128 * st;
-          const int* lm = sLim + 128 * st;
-          float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-          const int chunks = (t.cols + 31) >> 5;
+    while (ok) {
+      const int slot = nu % kRing;
+      ok = __all_sync(0xffffffffu, mbar_sleep(&u_full[slot], (nu / kRing) & 1, abort_flag, p.status));
+      if (!ok) break;
+      Unit x;
+      {
+        int* w = reinterpret_cast<int*>(&x);
+#pragma unroll
+        for (int i = 0; i < kUnitInts; ++i) w[i] = ring[slot * kUnitInts + i];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&u_empty[slot]);
+      ++nu;
+      if (x.nt < 0) break;
+      const int tile0 = x.key0 + 128 * s, key = tile0 + row;
+      const long long at = static_cast<long long>(x.bk * p.Hkv + x.hkv) * p.C + key;
+      const float before = p.Z == 1 && p.score_in && key < x.len ? p.score_in[at] : 0.f;
+      float acc = 0.f, comp = 0.f;
+      Tile t = {x.i, x.g, x.r0};
+      for (int f = 0; f < x.nt; ++f, ++qt) {
+        const int buf = qt & 1, st = qt % kLse;
+        const int cols = t.cols(p);
+        const bool mask = p.causal && tile0 + 127 > x.len - p.T + (p.by_head ? t.r0 : 0);
+        const uint32_t lh = (qt / kLse) & 1, sh = (qt >> 1) & 1;
+        const bool lr = mbar_try_wait(&l_full[st], lh), sr = mbar_try_wait(&s_full[2 * s + buf], sh);
+        ok = lr || mbar_sleep(&l_full[st], lh, abort_flag, p.status);
+        ok &= sr || mbar_sleep(&s_full[2 * s + buf], sh, abort_flag, p.status);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_after();
+        const float* nl = sLse + 128 * st;
+        const int* lm = sLim + 128 * st;
+        const uint32_t src = s_addr + 128 * buf;
+        float a[4] = {0.f, 0.f, 0.f, 0.f};
+        if (!mask && cols == 128) {
+          // 32 columns at a time, the next 32 on their way
+          float va[32], vb[32];
+          tmem_ld32(src, va);
+          tc_wait_ld();
+          tmem_ld32(src + 32, vb);
+          sum32(va, nl, p.scale_log2, a);
+          tc_wait_ld();
+          tmem_ld32(src + 64, va);
+          sum32(vb, nl + 32, p.scale_log2, a);
+          tc_wait_ld();
+          tmem_ld32(src + 96, vb);
+          sum32(va, nl + 64, p.scale_log2, a);
+          tc_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_empty[2 * s + buf]);
+          sum32(vb, nl + 96, p.scale_log2, a);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&l_empty[st]);
+        } else {
+          const int chunks = (cols + 31) >> 5;
 #pragma unroll 1
           for (int c = 0; c < chunks; ++c) {
             float v[32];
-            tmem_ld32(s_addr + 128 * buf + 32 * c, v);
+            tmem_ld32(src + 32 * c, v);
             tc_wait_ld();
-            if (mask || t.cols < 32 * (c + 1)) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const int col = 32 * c + i;
-                const float e = ex2_approx(fmaf(v[i], p.scale_log2, -ls[col]));
-                // a column that is no query of this tile has the limit -1
-                if (key <= lm[col]) a0 += e;
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const float4 l4 = *reinterpret_cast<const float4*>(ls + 32 * c + i);
-                float x0, x1, x2, x3;
-                ffma2(x0, x1, v[i], v[i + 1], p.scale_log2, p.scale_log2, -l4.x, -l4.y);
-                ffma2(x2, x3, v[i + 2], v[i + 3], p.scale_log2, p.scale_log2, -l4.z, -l4.w);
-                fadd2(a0, a1, a0, a1, ex2_approx(x0), ex2_approx(x1));
-                fadd2(a2, a3, a2, a3, ex2_approx(x2), ex2_approx(x3));
-              }
+            for (int i = 0; i < 32; ++i) {
+              const int col = 32 * c + i;
+              const float e = ex2_approx(fmaf(v[i], p.scale_log2, nl[col]));
+              // a column that is no query of this tile has the limit -1
+              if (key <= lm[col]) a[i & 3] += e;
             }
           }
           tc_fence_before();
@@ -444,24 +642,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&s_empty[2 * s + buf]);
             mbar_arrive(&l_empty[st]);
           }
-          // compensated: the tile's sum joins the key's
-          const float y = ((a0 + a1) + (a2 + a3)) - comp;
-          const float z = acc + y;
-          comp = (z - acc) - y;
-          acc = z;
         }
-        if (!ok) break;
-        if (key < p.C) {
-          if (p.Z > 1) {
-            const int z = u / (p.Bk * p.Hkv) % p.Z;
-            p.part[static_cast<long long>(z) * p.Bk * p.Hkv * p.C + at] = acc;
-          } else {
-            p.score_out[at] = key < x.len ? before + acc : 0.f;
-          }
+        // compensated: the tile's sum joins the key's
+        const float y = ((a[0] + a[1]) + (a[2] + a[3])) - comp;
+        const float z = acc + y;
+        comp = (z - acc) - y;
+        acc = z;
+        t.next(p, x);
+      }
+      if (!ok) break;
+      if (key < p.C) {
+        if (p.Z > 1) {
+          p.part[static_cast<long long>(x.z) * p.Bk * p.Hkv * p.C + at] = acc;
+        } else {
+          p.score_out[at] = key < x.len ? before + acc : 0.f;
         }
       }
-      u = un;
-      len = ln;
+    }
+    // units of a line end at the keys: the slots of the pairs behind them
+    if (!p.by_head && p.Z == 1) {
+      const int tid = threadIdx.x - 128;
+      const long long tail = static_cast<long long>(p.Bk) * p.Hkv * p.pairs;
+      for (long long u = blockIdx.x; u < tail; u += gridDim.x) {
+        const int bh = static_cast<int>(u / p.pairs), key = static_cast<int>(u - static_cast<long long>(bh) * p.pairs) * 256;
+        if (key >= clamped_len(p, bh / p.Hkv) && key + tid < p.C)
+          p.score_out[static_cast<long long>(bh) * p.C + key + tid] = 0.f;
+      }
     }
   }
 
@@ -471,6 +677,130 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
+}
+
+// ------------------------------------------------------------------ few queries
+constexpr int kStreamRows = 32;     // queries per key set and KV head, at most
+constexpr int kStreamThreads = 256;
+
+template <bool FP16>
+__device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+  if constexpr (FP16) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  } else {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
+}
+
+// NT: groups of eight queries.  A warp takes 16 keys a step; lane 4 g + t holds
+// pieces t, t + 4, .. (16 bytes each) of keys g and g + 8, and the same
+// pieces of query g of every group.
+template <int D, bool FP16, int NT>
+__global__ void __launch_bounds__(kStreamThreads, NT == 4 ? 1 : 2)
+    stream_kernel(const uint4* __restrict__ q, const uint4* __restrict__ k, const Params p, int chunk, int chunks) {
+  constexpr int kP = D / 32;  // pieces per lane and row
+  constexpr int kWarps = kStreamThreads / 32;
+  grid_dep_launch();
+  grid_dep_wait();
+  const int bh = blockIdx.x / chunks, c0 = (blockIdx.x - bh * chunks) * chunk;
+  const int bk = bh / p.Hkv, hkv = bh - bk * p.Hkv;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  if (blockIdx.x == 0) {
+    bool bad = false;
+    if (p.key_len)
+      for (int i = threadIdx.x; i < p.Bk; i += kStreamThreads) {
+        const int n = __ldg(p.key_len + i);
+        bad |= n < 0 || n > p.C;
+      }
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) *p.status = bad ? kStatusLength : 0;
+  }
+  const int len = clamped_len(p, bk);
+  const int end = min(c0 + chunk, p.C);
+  const long long base = static_cast<long long>(bh) * p.C;
+  const uint4* kb = k + base * (D / 8);
+  // K of the first step before anything else
+  uint4 cur[2][kP];
+  float sin = 0.f;
+  auto fetch = [&](int key0, uint4 (&f)[2][kP], float& si) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int key = key0 + g + 8 * h;
+#pragma unroll
+      for (int i = 0; i < kP; ++i)
+        f[h][i] = key < len ? __ldg(kb + static_cast<long long>(key) * (D / 8) + t + 4 * i) : make_uint4(0, 0, 0, 0);
+    }
+    // lanes t = 0 and 1 finish keys g and g + 8
+    const int key = key0 + g + 8 * t;
+    si = p.score_in && t < 2 && key < len ? p.score_in[base + key] : 0.f;
+  };
+  int key0 = c0 + 16 * warp;
+  if (key0 < min(end, len)) fetch(key0, cur, sin);
+  uint4 qf[NT][kP];
+  float nl[NT][2];
+  int lim[NT][2];
+  const int rows = p.n * p.GT;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int r = 8 * j + g;
+    const int i = r / p.GT, rr = r - i * p.GT;
+    const uint4* src = q + ((static_cast<long long>(bk * p.n + i) * p.Hkv + hkv) * p.GT + rr) * (D / 8);
+#pragma unroll
+    for (int m = 0; m < kP; ++m) qf[j][m] = r < rows ? __ldg(src + t + 4 * m) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r2 = 8 * j + 2 * t + e;
+      const int i2 = r2 / p.GT, rr2 = r2 - i2 * p.GT;
+      float l = -INFINITY;
+      if (r2 < rows) l = __ldg(p.lse + (static_cast<long long>(bk * p.n + i2) * p.Hkv + hkv) * p.GT + rr2);
+      // a query that saw nothing (lse -inf) adds nothing
+      nl[j][e] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+      lim[j][e] = r2 >= rows ? -1 : (p.causal ? len - p.T + rr2 % p.T : INT_MAX);
+    }
+  }
+  for (; key0 < min(end, len); key0 += 16 * kWarps) {
+    uint4 nxt[2][kP];
+    float sn = 0.f;
+    const int kn = key0 + 16 * kWarps;
+    if (kn < min(end, len)) fetch(kn, nxt, sn);
+    float w0 = 0.f, w1 = 0.f;  // keys g and g + 8
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int m = 0; m < kP; ++m) {
+        mma_16x8x16<FP16>(c, cur[0][m].x, cur[1][m].x, cur[0][m].y, cur[1][m].y, qf[j][m].x, qf[j][m].y);
+        mma_16x8x16<FP16>(c, cur[0][m].z, cur[1][m].z, cur[0][m].w, cur[1][m].w, qf[j][m].z, qf[j][m].w);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float e0 = ex2_approx(fmaf(c[e], p.scale_log2, nl[j][e]));
+        const float e1 = ex2_approx(fmaf(c[2 + e], p.scale_log2, nl[j][e]));
+        w0 += key0 + g <= lim[j][e] ? e0 : 0.f;
+        w1 += key0 + g + 8 <= lim[j][e] ? e1 : 0.f;
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      w0 += __shfl_xor_sync(0xffffffffu, w0, o);
+      w1 += __shfl_xor_sync(0xffffffffu, w1, o);
+    }
+    const int key = key0 + g + 8 * t;
+    if (t < 2 && key < end) p.score_out[base + key] = key < len ? sin + (t ? w1 : w0) : 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < kP; ++i) cur[h][i] = nxt[h][i];
+    sin = sn;
+  }
+  // slots of the chunk behind the last step
+  const int done = max(c0, len > c0 ? c0 + (min(end, len) - c0 + 15) / 16 * 16 : c0);
+  for (int key = done + threadIdx.x; key < end; key += kStreamThreads) p.score_out[base + key] = 0.f;
 }
 
 // score_out = score_in + the parts of a split unit, in order.
@@ -524,9 +854,8 @@ bool make_plan(Params& p, int B, int G, int Hkv, int T, int Bk, int C) {
   if (z > tiles / 4) z = tiles / 4;
   if (z > 16) z = 16;
   p.Z = z < 1 ? 1 : static_cast<int>(z);
-  if (units * p.Z > INT_MAX / 2) return false;
-  p.units = static_cast<int>(units * p.Z);
-  return true;
+  p.units = units * p.Z;
+  return units <= INT_MAX;
 }
 
 template <int D, bool FP16>
@@ -540,12 +869,31 @@ cudaError_t run(const Params& p, const CUtensorMap& mq, const CUtensorMap& mk, i
   return launch_chained(weight_sum_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, st, p);
 }
 
+bool streams(const Params& p) { return static_cast<long long>(p.n) * p.GT <= kStreamRows; }
+
+template <int D, bool FP16>
+cudaError_t run_stream(const WeightLaunch& a, const Params& p, cudaStream_t st) {
+  // keys per CTA: eight steps a warp, fewer while the grid is under two
+  // CTAs per SM twice over
+  const long long heads = static_cast<long long>(p.Bk) * p.Hkv;
+  int chunk = 1024;
+  while (chunk > 128 && heads * ((p.C + chunk - 1) / chunk) < 4 * kPlanSms) chunk /= 2;
+  const int chunks = (p.C + chunk - 1) / chunk;
+  const dim3 grid(static_cast<unsigned>(heads * chunks));
+  const uint4* q = static_cast<const uint4*>(a.q);
+  const uint4* k = static_cast<const uint4*>(a.k);
+  const int rows = p.n * p.GT;
+  if (rows <= 8) return launch_chained(stream_kernel<D, FP16, 1>, grid, dim3(kStreamThreads), 0, st, q, k, p, chunk, chunks);
+  if (rows <= 16) return launch_chained(stream_kernel<D, FP16, 2>, grid, dim3(kStreamThreads), 0, st, q, k, p, chunk, chunks);
+  return launch_chained(stream_kernel<D, FP16, 4>, grid, dim3(kStreamThreads), 0, st, q, k, p, chunk, chunks);
+}
+
 }  // namespace
 
 size_t weight_workspace_bytes(int B, int G, int Hkv, int T, int Bk, int C) {
   Params p = {};
   if (!make_plan(p, B, G, Hkv, T, Bk, C)) return 0;
-  const size_t part = p.Z > 1 ? static_cast<size_t>(p.Z) * Bk * Hkv * C * 4 : 0;
+  const size_t part = p.Z > 1 && !streams(p) ? static_cast<size_t>(p.Z) * Bk * Hkv * C * 4 : 0;
   return 256 + ((part + 255) & ~static_cast<size_t>(255));
 }
 
@@ -560,6 +908,10 @@ cudaError_t launch_weight(const WeightLaunch& a, cudaStream_t st) {
   p.scale_log2 = kLog2e / (a.d == 128 ? 11.313708498984761f : 8.0f);
   p.status = reinterpret_cast<int*>(a.ws);
   p.part = reinterpret_cast<float*>(a.ws + 256);
+  if (streams(p)) {
+    if (a.d == 128) return a.fp16 ? run_stream<128, true>(a, p, st) : run_stream<128, false>(a, p, st);
+    return a.fp16 ? run_stream<64, true>(a, p, st) : run_stream<64, false>(a, p, st);
+  }
   CUtensorMap mq, mk;
   const uint64_t u = 1;
   const uint64_t by_kv[4] = {u * a.d, u * p.GT, u * a.Hkv, u * a.B};
@@ -571,7 +923,7 @@ cudaError_t launch_weight(const WeightLaunch& a, cudaStream_t st) {
       encode_tensor_map_16(&mk, a.k, a.fp16, 3, dk, bk) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   int grid = device_sm_count();
-  if (p.units < grid) grid = p.units;
+  if (p.units < grid) grid = static_cast<int>(p.units);
   if (a.d == 128) return a.fp16 ? run<128, true>(p, mq, mk, grid, st) : run<128, false>(p, mq, mk, grid, st);
   return a.fp16 ? run<64, true>(p, mq, mk, grid, st) : run<64, false>(p, mq, mk, grid, st);
 }
