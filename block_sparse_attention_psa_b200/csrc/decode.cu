@@ -79,7 +79,8 @@ struct Params {
   int own_rb, own_rt, own_up;
   float scale_log2;
   long long pre_slots; // slots of the prefix region: the caches' parts start behind it
-  long long* seg_off;  // [npre + 1] and [caches + 1]: first place of each segment on its line, then the line's length
+  long long own_unit0; // place of the caches' units in unit_ctas
+  int2* unit_ctas;     // per unit: the CTAs that have its first and its last key tile
   float* part_o;       // parts: rows x d
   float2* part_ml;     // reference (log2 units), sum
   int* status;
@@ -241,11 +242,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     long long total = 0;
     for (int w = 0; w < kThreads / 32; ++w) total += red[w];
-    x0[line] = total * blockIdx.x / gridDim.x;
-    x1[line] = total * (blockIdx.x + 1) / gridDim.x;
-    if (blockIdx.x == 0 && threadIdx.x == 0) p.seg_off[sb + line] = total;
+    // no empty runs between others: every CTA between a unit's first and its
+    // last one writes that unit's parts
+    const long long g = min(total, static_cast<long long>(gridDim.x)), c = blockIdx.x;
+    x0[line] = c < g ? total * c / g : 0;
+    x1[line] = c < g ? total * (c + 1) / g : 0;
     long long run = 0;
-    for (int s0 = sa; s0 < sb && (x0[line] < x1[line] || blockIdx.x == 0); s0 += kThreads) {
+    for (int s0 = sa; s0 < sb && x0[line] < x1[line]; s0 += kThreads) {
       const int s = s0 + threadIdx.x;
       const long long t = s < sb ? seg_work(p, s) : 0;
       long long inc = t;
@@ -267,7 +270,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         start_seg[line] = s;
         start_off[line] = lo;
       }
-      if (blockIdx.x == 0 && s < sb) p.seg_off[s + line] = lo;
     }
   }
   bad = __syncthreads_or(bad);
@@ -314,9 +316,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         c.j0 = static_cast<int>(tiles_before(x, o0, 1 + c.pair));
         c.nt = static_cast<int>(tiles_before(min(o1, xe), o0, 1 + c.pair)) - c.j0;
         x = min(o1, xe);
-        if (c.nt == 0) continue;  // the rest of a tile that the run before took
         c.len = len;
-        c.slot = c.outer * p.Hkv * up + lu + static_cast<int>(blockIdx.x);
+        const int unit = c.outer * p.Hkv * up + lu;
+        c.slot = unit + static_cast<int>(blockIdx.x);
+        if (c.nt == 0) {
+          // the rest of a tile that the run before took: parts without terms
+          const int rows = 2 * (pre ? p.pre_nb * p.pre_rb : p.own_rb);
+          float2* ml = p.part_ml + (pre ? 0 : p.pre_slots) + static_cast<long long>(c.slot) * rows;
+          for (int i = lane; i < rows; i += 32) ml[i] = make_float2(-INFINITY, 0.f);
+          continue;
+        }
+        if (lane == 0) {
+          int2* uc = p.unit_ctas + (pre ? 0 : p.own_unit0) + unit;
+          if (c.j0 == 0) uc->x = static_cast<int>(blockIdx.x);
+          if (c.j0 + c.nt == nkt) uc->y = static_cast<int>(blockIdx.x);
+        }
         c.tiles = tiles;
         c.items = items;
         c.qpos = qpos;
@@ -555,7 +569,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++np;
       if (c.nt == 0) break;
       const int sub = s ^ (c.items & 1);
-      if (!c.pair && sub >= c.nt) continue;  // a single tile: the other stream's
+      if (!c.pair && sub >= c.nt) {
+        // a single tile, the other stream's: a part without terms
+        const int stride = c.prefix ? p.pre_nb * p.pre_rb : p.own_rb;
+        if (x < stride)
+          p.part_ml[(c.prefix ? 0 : p.pre_slots) + (static_cast<long long>(c.slot) * 2 + sub) * stride + x] =
+              make_float2(-INFINITY, 0.f);
+        continue;
+      }
       const int tile = c.tile0 + (c.pair ? sub : 0);
       // this thread's row
       int r;
@@ -696,108 +717,103 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------ merge
 // One output row per block: with M the largest reference of its parts,
 //   out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p.
-// The parts of a row are found from the schedule alone (segment offsets and
-// grid size); warps take them in turn, and the order of the sums is fixed.
+// All references are read at once, then the rows of O with their weights
+// known, several in flight per warp; the order of the sums is fixed.
 constexpr int kMergeThreads = 128;
+constexpr int kMaxParts = 4 * kMaxCtas;  // two per CTA from the prefix, two from the cache
 
 template <int D, bool FP16>
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p, int grid, uint16_t* out, float* lse) {
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p, uint16_t* out, float* lse) {
   constexpr int kV = D / 32;  // values per lane
+  __shared__ float w[kMaxParts];
+  __shared__ int at[kMaxParts];
   __shared__ float so[4][D];
-  __shared__ float2 sml[4];
+  __shared__ float red[4];
   grid_dep_launch();
   grid_dep_wait();
   const int row = blockIdx.x;  // (b, hkv, r)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bh = row / p.GT, r = row - bh * p.GT;
   const int b = bh / p.Hkv, hkv = bh - b * p.Hkv;
-  float acc[kV];
+  // where the row's parts are: first CTA, count and place of the first
+  int cnt[2] = {0, 0}, first[2] = {0, 0}, step[2] = {0, 0};
 #pragma unroll
-  for (int i = 0; i < kV; ++i) acc[i] = 0.f;
-  float m = -INFINITY, l = 0.f;
-  int turn = 0;
   for (int half = 0; half < 2; ++half) {
     // half 0: the prefix, 1: the cache
     if (half == 0 ? p.npre == 0 : p.nseg == p.npre) continue;
-    const int seg = half == 0 ? b / p.n : p.npre + b;
-    const long long off = p.seg_off[seg + half], W = p.seg_off[half == 0 ? p.npre : p.nseg + 1];
+    const int outer = half == 0 ? b / p.n : b;
+    if (seg_len(p, half == 0 ? outer : p.npre + b) == 0) continue;
     const int up = half == 0 ? p.pre_up : p.own_up, rt = half == 0 ? p.pre_rt : p.own_rt;
-    const int nkt = static_cast<int>((p.seg_off[seg + half + 1] - off) / (p.Hkv * rt));
-    if (nkt == 0) continue;
-    int tile, x, stride;
-    if (half == 0) {
-      const int i = b - seg * p.n;
-      stride = p.pre_nb * p.pre_rb;
-      if (p.GT >= 128) {
-        tile = i * ((p.GT + 127) / 128) + r / 128;
-        x = r % 128;
-      } else {
-        tile = i / p.pre_nb;
-        x = (i - tile * p.pre_nb) * p.GT + r;
-      }
+    const int stride = half == 0 ? p.pre_nb * p.pre_rb : p.own_rb;
+    int tile, x;
+    if (half == 0 && p.GT < 128) {
+      const int i = b - outer * p.n;
+      tile = i / p.pre_nb;
+      x = (i - tile * p.pre_nb) * p.GT + r;
     } else {
-      stride = p.own_rb;
-      tile = r / 128;
+      tile = r / 128 + (half == 0 ? (b - outer * p.n) * ((p.GT + 127) / 128) : 0);
       x = r % 128;
     }
-    const int lu = hkv * up + (tile >> 1);
     const bool pair = (tile | 1) < rt;
-    const int w = pair ? 2 : 1;
-    const long long o0 = off + (static_cast<long long>(hkv) * rt + (tile & ~1)) * nkt;
-    const long long o1 = o0 + static_cast<long long>(w) * nkt;
-    const int c0 = static_cast<int>(((o0 + 1) * grid - 1) / W), c1 = static_cast<int>((o1 * grid - 1) / W);
-    const long long unit = static_cast<long long>(half == 0 ? seg : b) * p.Hkv * up + lu;
-    const long long base = half == 0 ? 0 : p.pre_slots;
-    const int nsub = pair ? 1 : 2;
-    for (int q = (warp - turn) & 3; q < (c1 - c0 + 1) * nsub; q += 4) {
-      const int c = c0 + (pair ? q : q >> 1);
-      const int sub = pair ? (tile & 1) : (q & 1);
-      const long long lo = tiles_before(max(o0, W * c / grid), o0, w);
-      const long long hi = tiles_before(min(o1, W * (c + 1) / grid), o0, w);
-      if (hi <= lo || (!pair && sub >= hi - lo)) continue;
-      const long long at = base + ((unit + c) * 2 + sub) * stride + x;
-      const float2 ml = p.part_ml[at];
-      float v[kV];
-      const float* src = p.part_o + at * D + lane * kV;
-      if constexpr (kV == 4) {
-        const float4 f = *reinterpret_cast<const float4*>(src);
-        v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-      } else {
-        const float2 f = *reinterpret_cast<const float2*>(src);
-        v[0] = f.x, v[1] = f.y;
-      }
-      if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing visible in this part
-      const float mn = fmaxf(m, ml.x);
-      const float fa = m == -INFINITY ? 0.f : ex2_approx(m - mn);
-      const float fb = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mn);
-      m = mn;
-      l = l * fa + ml.y * fb;
-#pragma unroll
-      for (int i = 0; i < kV; ++i) acc[i] = acc[i] * fa + v[i] * fb;
-    }
-    turn += (c1 - c0 + 1) * nsub;
+    const int unit = (outer * p.Hkv + hkv) * up + (tile >> 1);
+    const int2 c = p.unit_ctas[(half == 0 ? 0 : p.own_unit0) + unit];
+    // a pair's row has one part per CTA (stream tile & 1), another's two
+    cnt[half] = (c.y - c.x + 1) * (pair ? 1 : 2);
+    step[half] = pair ? 2 * stride : stride;
+    first[half] = static_cast<int>((half == 0 ? 0 : p.pre_slots) + 2LL * (unit + c.x) * stride +
+                                   (pair ? (tile & 1) * stride : 0)) + x;
   }
-  if (lane == 0) sml[warp] = make_float2(m, l);
+  const int n = cnt[0] + cnt[1];
+  float M = -INFINITY;
+  for (int q = threadIdx.x; q < n; q += kMergeThreads) {
+    const int a = q < cnt[0] ? first[0] + q * step[0] : first[1] + (q - cnt[0]) * step[1];
+    at[q] = a;
+    M = fmaxf(M, p.part_ml[a].x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) red[warp] = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  float L = 0.f;
+  for (int q = threadIdx.x; q < n; q += kMergeThreads) {
+    const float2 ml = p.part_ml[at[q]];
+    // nothing visible in this part: weight 0, and its O is not read
+    const float f = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2_approx(ml.x - M);
+    w[q] = f;
+    if (f != 0.f) L += f * ml.y;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  __syncthreads();
+  if (lane == 0) red[warp] = L;
+  __syncthreads();
+  L = (red[0] + red[1]) + (red[2] + red[3]);
+  float acc[kV];
+#pragma unroll
+  for (int i = 0; i < kV; ++i) acc[i] = 0.f;
+#pragma unroll 4
+  for (int q = warp; q < n; q += 4) {
+    const float f = w[q];
+    if (f != 0.f) {
+      const float* src = p.part_o + static_cast<long long>(at[q]) * D + lane * kV;
+      if constexpr (kV == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        acc[0] += f * v.x, acc[1] += f * v.y, acc[2] += f * v.z, acc[3] += f * v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        acc[0] += f * v.x, acc[1] += f * v.y;
+      }
+    }
+  }
 #pragma unroll
   for (int i = 0; i < kV; ++i) so[warp][lane * kV + i] = acc[i];
   __syncthreads();
-  float M = -INFINITY, L = 0.f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) M = fmaxf(M, sml[w].x);
-  float f[4];
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    f[w] = sml[w].x == -INFINITY && sml[w].y == 0.f ? 0.f : ex2_approx(sml[w].x - M);
-    L += f[w] * sml[w].y;
-  }
   const bool empty = M == -INFINITY && L == 0.f;
-  for (int i = 2 * threadIdx.x; i < D; i += 2 * kMergeThreads) {
-    float a0 = 0.f, a1 = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      a0 += f[w] * so[w][i];
-      a1 += f[w] * so[w][i + 1];
-    }
+  const int i = 2 * threadIdx.x;
+  if (i < D) {
+    const float a0 = (so[0][i] + so[1][i]) + (so[2][i] + so[3][i]);
+    const float a1 = (so[0][i + 1] + so[1][i + 1]) + (so[2][i + 1] + so[3][i + 1]);
     const uint32_t u = empty ? 0u : pack_16x2<FP16>(a0 / L, a1 / L);
     *reinterpret_cast<uint32_t*>(out + static_cast<long long>(row) * D + i) = u;
   }
@@ -809,7 +825,7 @@ size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 struct Plan {
   Params p = {};
   long long pre_units = 0, own_units = 0, part_rows = 0;
-  size_t off_seg = 0, off_ml = 0, off_o = 0, total = 0;
+  size_t off_units = 0, off_ml = 0, off_o = 0, total = 0;
 };
 
 // Everything that follows from the sizes alone.
@@ -843,11 +859,13 @@ bool make_plan(Plan& w, int B, int G, int Hkv, int T, int d, int Bp, int P, int 
   w.own_units = C > 0 ? static_cast<long long>(B) * Hkv * p.own_up : 0;
   const long long tiles = w.pre_units * ((P + 127LL) / 128) + w.own_units * ((C + 127LL) / 128);
   if (w.pre_units + w.own_units > (1LL << 30) || tiles > (1LL << 50)) return false;
+  p.own_unit0 = w.pre_units;
   p.pre_slots = P > 0 ? (w.pre_units + kMaxCtas) * 2 * p.pre_nb * p.pre_rb : 0;
   w.part_rows = p.pre_slots + (C > 0 ? (w.own_units + kMaxCtas) * 2 * p.own_rb : 0);
+  if (w.part_rows >= (1LL << 31)) return false;
   size_t o = 256;
-  w.off_seg = o;
-  o += align256(static_cast<size_t>(p.nseg + 2) * 8);
+  w.off_units = o;
+  o += align256(static_cast<size_t>(w.pre_units + w.own_units) * 8);
   w.off_ml = o;
   o += align256(static_cast<size_t>(w.part_rows) * 8);
   w.off_o = o;
@@ -865,7 +883,7 @@ cudaError_t run(const DecodeLaunch& a, const Plan& w, const CUtensorMap (&m)[6],
                                         m[1], m[2], m[3], m[4], m[5], w.p);
   if (e2 != cudaSuccess) return e2;
   return launch_chained(merge_kernel<D, FP16>, dim3(static_cast<unsigned>(a.B) * a.Hkv * w.p.GT), dim3(kMergeThreads),
-                        0, st, w.p, grid, static_cast<uint16_t*>(a.out), a.lse);
+                        0, st, w.p, static_cast<uint16_t*>(a.out), a.lse);
 }
 
 }  // namespace
@@ -883,7 +901,7 @@ cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t st) {
   p.cache_len = a.cache_len;
   p.scale_log2 = 1.4426950408889634f / (a.d == 128 ? 11.313708498984761f : 8.0f);
   p.status = reinterpret_cast<int*>(a.ws);
-  p.seg_off = reinterpret_cast<long long*>(a.ws + w.off_seg);
+  p.unit_ctas = reinterpret_cast<int2*>(a.ws + w.off_units);
   p.part_ml = reinterpret_cast<float2*>(a.ws + w.off_ml);
   p.part_o = reinterpret_cast<float*>(a.ws + w.off_o);
   // Q: [B][Hkv][G T][d]; prefix tiles take pre_nb sequences at once

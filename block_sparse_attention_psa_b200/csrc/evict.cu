@@ -56,60 +56,60 @@ __device__ __forceinline__ uint32_t score_key(float f) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// Exclusive prefix over the cluster's CTAs of one int per CTA, and the total.
-// `box` is written and read by this call alone.
-__device__ __forceinline__ int cluster_exclusive(cg::cluster_group& cl, int* box, int mine, int& total) {
-  if (threadIdx.x == 0) *box = mine;
-  cl.sync();
-  int before = 0;
-  total = 0;
-  for (unsigned r = 0; r < cl.num_blocks(); ++r) {
-    const int v = *cl.map_shared_rank(box, r);
-    if (r < cl.block_rank()) before += v;
-    total += v;
-  }
-  return before;
-}
-
-// Exclusive prefix over the block's warps of a warp-uniform value, and the
-// block's total.  `buf` holds 33 ints.
-__device__ __forceinline__ int warps_exclusive(int* buf, int mine, int& total) {
+// Exclusive prefix over the block's warps of two warp-uniform counts, and the
+// block's totals.  `buf` holds 33 pairs.
+__device__ __forceinline__ int2 warps_exclusive(int2* buf, int2 mine, int2& total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   __syncthreads();
   if (lane == 0) buf[warp] = mine;
   __syncthreads();
-  if (warp == 0) {
-    const int v = lane < warps ? buf[lane] : 0;
-    int s = v;
+  // every warp scans for itself: no third barrier
+  int2 v = lane < warps ? buf[lane] : make_int2(0, 0), s = v;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += u;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int ux = __shfl_up_sync(0xffffffffu, s.x, o), uy = __shfl_up_sync(0xffffffffu, s.y, o);
+    if (lane >= o) {
+      s.x += ux;
+      s.y += uy;
     }
-    __syncwarp();
-    buf[lane] = s - v;
-    if (lane == 31) buf[32] = s;
   }
-  __syncthreads();
-  total = buf[32];
-  return buf[warp];
+  total = make_int2(__shfl_sync(0xffffffffu, s.x, 31), __shfl_sync(0xffffffffu, s.y, 31));
+  return make_int2(__shfl_sync(0xffffffffu, s.x - v.x, warp), __shfl_sync(0xffffffffu, s.y - v.y, warp));
 }
 
+// Shared by the cluster's CTAs (each reads the others').
+struct SelectShared {
+  uint32_t hist[3][kBins];  // one per round: nothing is cleared while it may still be read
+  int2 count[2];            // totals of a CTA, one per exchange
+  int last;                 // latest position
+};
+
+// CL: the head is split over a cluster; else one CTA has it all and the
+// cluster's barriers are the block's.
+template <bool CL>
 __global__ void __launch_bounds__(kMaxThreads, 1) select_kernel(const SelectParams p) {
-  extern __shared__ uint32_t smem[];
-  __shared__ uint32_t hist[kBins];
-  __shared__ uint32_t sum[kBins];
-  __shared__ int buf[33];
-  __shared__ int box[4];
-  __shared__ uint32_t pick[2];  // chosen bin, keys above it
+  extern __shared__ __align__(16) uint32_t smem[];
+  __shared__ __align__(16) SelectShared sh;
+  __shared__ int2 buf[33];
+  __shared__ uint32_t wsum[32];
+  __shared__ uint32_t pick[3];  // chosen bin, keys above it, keys in it
   cg::cluster_group cl = cg::this_cluster();
-  const int rank = static_cast<int>(cl.block_rank());
-  const int ncta = static_cast<int>(cl.num_blocks());
+  const int rank = CL ? static_cast<int>(cl.block_rank()) : 0;
+  const int ncta = CL ? static_cast<int>(cl.num_blocks()) : 1;
+  auto sync_all = [&]() {
+    if constexpr (CL) {
+      cl.sync();
+    } else {
+      __syncthreads();
+    }
+  };
+  auto peer = [&](int r) -> const SelectShared* { return CL ? cl.map_shared_rank(&sh, r) : &sh; };
   const int bh = blockIdx.x / ncta;
   const int b = bh / p.Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x;
   uint32_t* stay = smem;                      // one bit per slot of the slice
   uint32_t* keys = smem + (p.slice >> 5);     // the slice's keys (when they fit)
+  for (int i = tid; i < 3 * kBins / 4; i += nthr) reinterpret_cast<uint4*>(&sh.hist[0][0])[i] = make_uint4(0, 0, 0, 0);
   grid_dep_launch();
   grid_dep_wait();
 
@@ -142,50 +142,50 @@ __global__ void __launch_bounds__(kMaxThreads, 1) select_kernel(const SelectPara
   // ---- the latest position of the head
   const int s0 = rank * p.slice, s1 = min(s0 + p.slice, len);
   int last = len - 1;
-  if (pos) {
+  if (pos && p.recent > 0) {
     last = INT_MIN;
+#pragma unroll 8
     for (int i = s0 + tid; i < s1; i += nthr) last = max(last, __ldg(pos + i));
     last = __reduce_max_sync(0xffffffffu, last);
-    if (lane == 0) buf[warp] = last;
+    if (lane == 0) buf[warp].x = last;
     __syncthreads();
-    if (tid == 0) {
-      for (int w = 1; w < (nthr >> 5); ++w) last = max(last, buf[w]);
-      box[0] = last;
+    last = __reduce_max_sync(0xffffffffu, lane < (nthr >> 5) ? buf[lane].x : INT_MIN);
+    if constexpr (CL) {
+      if (tid == 0) sh.last = last;
+      cl.sync();
+      last = __reduce_max_sync(0xffffffffu, lane < ncta ? peer(lane)->last : INT_MIN);
     }
-    cl.sync();
-    for (int r = 0; r < ncta; ++r) last = max(last, *cl.map_shared_rank(&box[0], r));
-    last = __shfl_sync(0xffffffffu, last, 0);
   }
   // positions after `last - recent` are protected; 64 bits, so that no
   // position a caller stores can wrap it
-  const long long guard = static_cast<long long>(last) - p.recent;
+  const long long guard = p.recent > 0 ? static_cast<long long>(last) - p.recent : LLONG_MAX;
   auto make_key = [&](int i) -> uint32_t {
     const int at = pos ? __ldg(pos + i) : i;
-    if (at < p.sink || at > guard) return 0xffffffffu;
-    return score_key(__ldg(score + i));
+    const uint32_t k = score_key(__ldg(score + i));
+    return at < p.sink || at > guard ? 0xffffffffu : k;
   };
-  if (p.keys_on_chip)
+  if (p.keys_on_chip) {
+#pragma unroll 8
     for (int i = s0 + tid; i < s1; i += nthr) keys[i - s0] = make_key(i);
+  }
   auto key = [&](int i) -> uint32_t { return p.keys_on_chip ? keys[i - s0] : make_key(i); };
   __syncthreads();
 
   // ---- radix select of the nk-th largest key
-  uint32_t prefix = 0, need = static_cast<uint32_t>(nk);
-#pragma unroll
+  uint32_t prefix = 0, need = static_cast<uint32_t>(nk), equal = 0;
+#pragma unroll 1
   for (int round = 0; round < 3; ++round) {
     const int shift = round == 0 ? 21 : (round == 1 ? 10 : 0);
     const int bits = round == 2 ? 10 : 11;
-    const int above = shift + bits;  // bits already decided start here
     const uint32_t mask = (1u << bits) - 1u;
-    for (int i = tid; i < kBins; i += nthr) hist[i] = 0u;
-    __syncthreads();
+    uint32_t* hist = sh.hist[round];
     const int trips = (s1 - s0 + nthr - 1) / nthr;
     for (int it = 0; it < trips; ++it) {
       const int i = s0 + it * nthr + tid;
       uint32_t bin = 0xffffffffu;
       if (i < s1) {
         const uint32_t k = key(i);
-        if (round == 0 || (k >> above) == prefix) bin = (k >> shift) & mask;
+        if (round == 0 || (k >> (shift + bits)) == prefix) bin = (k >> shift) & mask;
       }
       // a warp whose keys share one bin (equal scores) adds once
       int same;
@@ -196,88 +196,100 @@ __global__ void __launch_bounds__(kMaxThreads, 1) select_kernel(const SelectPara
         atomicAdd(&hist[bin], 1u);
       }
     }
-    cl.sync();
-    for (int i = tid; i < kBins; i += nthr) {
-      uint32_t s = 0;
-      for (int r = 0; r < ncta; ++r) s += *cl.map_shared_rank(&hist[i], r);
-      sum[i] = s;
-    }
-    cl.sync();  // the remote histograms may be cleared again (and sum[] is complete)
-    // bins from the top: the first warp scans 64 per lane
-    if (warp == 0) {
-      constexpr int kPer = kBins / 32;
-      uint32_t s = 0;
-      for (int j = 0; j < kPer; ++j) s += sum[kBins - 1 - (lane * kPer + ((j + lane) % kPer))];
-      uint32_t inc = s;
+    sync_all();
+    // thread t has the bins [kBins - per (t + 1), kBins - per t): counts above
+    // them by a scan, and the bin where the count passes `need`
+    const int per = kBins / nthr;
+    const int low = kBins - per * (tid + 1);
+    uint32_t mine = 0;
+    for (int j = 0; j < per; ++j)
+      for (int r = 0; r < ncta; ++r) mine += peer(r)->hist[round][low + j];
+    uint32_t inc = mine;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += u;
-      }
-      uint32_t at = inc - s;  // keys in the bins above this lane's
-      if (at < need && need <= inc) {
-        for (int j = 0; j < kPer; ++j) {
-          const int bin = kBins - 1 - (lane * kPer + j);
-          if (at + sum[bin] >= need) {
-            pick[0] = static_cast<uint32_t>(bin);
-            pick[1] = at;
-            break;
-          }
-          at += sum[bin];
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    uint32_t at = inc - mine;
+    for (int w = 0; w < warp; ++w) at += wsum[w];
+    if (at < need && need <= at + mine) {
+      for (int j = per - 1; j >= 0; --j) {
+        uint32_t n = 0;
+        for (int r = 0; r < ncta; ++r) n += peer(r)->hist[round][low + j];
+        if (at + n >= need) {
+          pick[0] = static_cast<uint32_t>(low + j);
+          pick[1] = at;
+          pick[2] = n;
+          break;
         }
+        at += n;
       }
     }
     __syncthreads();
     prefix = (prefix << bits) | pick[0];
     need -= pick[1];
-    __syncthreads();
+    equal = pick[2];
+    // (the next round's barrier keeps `pick` and `wsum` until all have read)
   }
-  // prefix is K*; `need` entries with that key stay
+  // prefix is K*; of the `equal` entries with that key the first `need` stay
 
   // ---- which entries stay; each warp owns the slots [w0, w1)
   const int per_warp = p.slice / (nthr >> 5);
   const int w0 = min(s0 + warp * per_warp, s1), w1 = min(w0 + per_warp, s1);
-  int eq = 0;
-  for (int i = w0 + lane; i - lane < w1; i += 32)
-    eq += __popc(__ballot_sync(0xffffffffu, i < w1 && key(i) == prefix));
-  int total, all;
-  int eq_at = warps_exclusive(buf, eq, total);
-  eq_at += cluster_exclusive(cl, &box[1], total, all);
-  int holes = 0, lates = 0;
+  int2 total;
+  int eq_at = 0;
+  if (need < equal) {  // the same everywhere: ties are cut, so they are ranked
+    int eq = 0;
+    for (int i = w0 + lane; i - lane < w1; i += 32)
+      eq += __popc(__ballot_sync(0xffffffffu, i < w1 && key(i) == prefix));
+    eq_at = warps_exclusive(buf, make_int2(eq, 0), total).x;
+    if constexpr (CL) {
+      if (tid == 0) sh.count[0] = total;
+      cl.sync();
+      for (int r = 0; r < rank; ++r) eq_at += peer(r)->count[0].x;
+    }
+  }
+  int2 n = make_int2(0, 0);  // holes, late survivors
   for (int i = w0 + lane; i - lane < w1; i += 32) {
     const uint32_t k = i < w1 ? key(i) : 0u;
     const uint32_t tie = __ballot_sync(0xffffffffu, i < w1 && k == prefix);
     const int before = eq_at + __popc(tie & ((1u << lane) - 1u));
-    const bool in = i < w1 && (k > prefix || (k == prefix && before < static_cast<int>(need)));
+    const bool in = i < w1 && (k > prefix || (k == prefix && (need == equal || before < static_cast<int>(need))));
     eq_at += __popc(tie);
     const uint32_t word = __ballot_sync(0xffffffffu, in);
     if (lane == 0) stay[(i - s0) >> 5] = word;
-    holes += __popc(__ballot_sync(0xffffffffu, i < w1 && i < nk && !in));
-    lates += __popc(__ballot_sync(0xffffffffu, in && i >= nk));
+    n.x += __popc(__ballot_sync(0xffffffffu, i < w1 && i < nk && !in));
+    n.y += __popc(__ballot_sync(0xffffffffu, in && i >= nk));
   }
-  int hole_at = warps_exclusive(buf, holes, total);
-  hole_at += cluster_exclusive(cl, &box[2], total, all);
-  int late_at = warps_exclusive(buf, lates, total);
-  late_at += cluster_exclusive(cl, &box[3], total, all);
+  int2 base = warps_exclusive(buf, n, total);
+  if constexpr (CL) {
+    if (tid == 0) sh.count[1] = total;
+    cl.sync();
+    for (int r = 0; r < rank; ++r) {
+      const int2 c = peer(r)->count[1];
+      base.x += c.x;
+      base.y += c.y;
+    }
+  }
   __syncwarp();
+  int at = base.y;
   for (int i = w0 + lane; i - lane < w1; i += 32) {
-    const uint32_t word = stay[(i - s0) >> 5];
-    const bool in = (word >> lane) & 1u;
+    const bool in = (stay[(i - s0) >> 5] >> lane) & 1u;
     const uint32_t far = __ballot_sync(0xffffffffu, in && i >= nk);
-    if (in && i >= nk) late[late_at + __popc(far & ((1u << lane) - 1u))] = i;
-    late_at += __popc(far);
-  }
-  cl.sync();  // orders the list's global writes for the cluster
-  for (int i = w0 + lane; i - lane < w1; i += 32) {
-    const uint32_t word = stay[(i - s0) >> 5];
-    const bool in = (word >> lane) & 1u;
-    const bool hole = i < w1 && i < nk && !in;
-    const uint32_t open = __ballot_sync(0xffffffffu, hole);
-    if (hole) kept[i] = *(volatile int*)(late + hole_at + __popc(open & ((1u << lane) - 1u)));
+    if (in && i >= nk) late[at + __popc(far & ((1u << lane) - 1u))] = i;
+    at += __popc(far);
     if (in && i < nk) kept[i] = i;
-    hole_at += __popc(open);
   }
-  cl.sync();  // no CTA leaves while another may read its shared memory
+  sync_all();  // orders the list's global writes; nobody reads another's shared memory after it
+  at = base.x;
+  for (int i = w0 + lane; i - lane < min(w1, nk); i += 32) {
+    const bool hole = i < w1 && i < nk && !((stay[(i - s0) >> 5] >> lane) & 1u);
+    const uint32_t open = __ballot_sync(0xffffffffu, hole);
+    if (hole) kept[i] = *(volatile int*)(late + at + __popc(open & ((1u << lane) - 1u)));
+    at += __popc(open);
+  }
 }
 
 struct MoveParams {
@@ -363,21 +375,22 @@ cudaError_t launch_evict(const EvictLaunch& a, cudaStream_t st) {
   s.budget = a.budget;
   s.sink = a.sink;
   s.recent = a.recent;
-  // CTAs per head: slices of about 4096 slots, while the heads alone do not
+  // CTAs per head: slices of about 8192 slots, while the heads alone do not
   // fill the machine (a cluster costs its barriers); 8 is the portable limit
   const long long heads = static_cast<long long>(a.B) * a.Hkv;
   int ncta = 1;
-  while (ncta < 8 && a.C > 4096 * ncta && heads * ncta * 2 <= 296) ncta *= 2;
+  while (ncta < 8 && a.C > 8192 * ncta && heads * ncta * 2 <= 296) ncta *= 2;
   while (ncta < 8 && (a.C + ncta - 1) / ncta > kSmemKeys) ncta *= 2;
   const int part = (a.C + ncta - 1) / ncta;
-  int threads = kMaxThreads;
+  // four slots or more per thread; two CTAs per SM when there are more heads than SMs
+  int threads = heads * ncta > 148 ? kMaxThreads / 2 : kMaxThreads;
   while (threads > 128 && threads * 4 > part) threads /= 2;
   s.slice = (part + threads - 1) / threads * threads;
   s.keys_on_chip = s.slice <= kSmemKeys;
   const size_t smem = static_cast<size_t>(s.slice / 32 + (s.keys_on_chip ? s.slice : 0)) * 4;
+  auto kernel = ncta > 1 ? select_kernel<true> : select_kernel<false>;
   cudaError_t e = cudaSuccess;
-  if (smem > 24 * 1024)
-    e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 180 * 1024);
+  if (smem > 20 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 180 * 1024);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(heads * ncta));
@@ -392,8 +405,8 @@ cudaError_t launch_evict(const EvictLaunch& a, cudaStream_t st) {
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  if ((e = cudaLaunchKernelEx(&cfg, select_kernel, s)) != cudaSuccess) return e;
+  cfg.numAttrs = ncta > 1 ? 2 : 1;
+  if ((e = cudaLaunchKernelEx(&cfg, kernel, s)) != cudaSuccess) return e;
 
   MoveParams m = {};
   m.k = reinterpret_cast<const uint4*>(a.k);

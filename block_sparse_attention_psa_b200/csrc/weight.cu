@@ -8,7 +8,10 @@
 // operands K-major in shared memory): a thread owns one TMEM lane, i.e. one
 // key, so a key's sum runs inside a thread and needs no exchange.  The lse of
 // the queries runs along the columns and is read from shared memory, four
-// columns per broadcast load.
+// columns per broadcast load; lse_kernel lays it out beforehand as the tiles
+// want it (-lse log2 e, -inf in columns without a query), so that a tile's
+// 512 bytes come with one bulk copy.  (A warp that gathered them itself was what
+// a 64-token window waited for: 7000 cycles a unit.)
 //
 //  * Decode reads K once for few queries: bound by DRAM.  A prefill does 2 d
 //    operations and one exponential per (query, key) pair: an SM's tensor
@@ -21,9 +24,12 @@
 //    stands between the loads; the legacy tensor path has an order of
 //    magnitude to spare at this ratio.
 //  * More: weight_kernel. Unit: a pair of key tiles (256 keys) of one KV head,
-//    held in shared memory, with the query tiles streamed past it; each of the
-//    two warpgroups owns one key tile, so a query tile is loaded once for
-//    both, and each has two S buffers (512 TMEM columns in all). One warp
+//    held in shared memory, with the query tiles streamed past it, so that a
+//    query tile is loaded once for both key tiles; each key tile has two S
+//    buffers (512 TMEM columns in all) and two warpgroups that take half the
+//    columns each, four warps per scheduler in all (with two, a tile took 2700
+//    cycles instead of ~1900: loads from TMEM, waits and chains of the
+//    polynomial were exposed).  One warp
 //    works out the units and publishes them; the others only step through
 //    them (divisions in every role had cost more than the products).
 //  * Query tiles: T >= 128 tokens: 128 tokens of one head, so that causal
@@ -47,13 +53,13 @@
 namespace psa {
 namespace {
 
-constexpr int kThreads = 384;      // WG0: K/Q loads, MMA issue, lse loads, units; WG1, WG2: one key tile each
-constexpr int kRegsProducer = 72;  // 128 x 72 + 256 x 216 = 384 x 168
-constexpr int kRegsSum = 216;
+constexpr int kThreads = 640;      // WG0: K/Q loads, MMA issue, lse loads, units; WG1..4: half the columns of a key tile each
+constexpr int kRegsProducer = 64;  // 128 x 64 + 512 x 104 = 640 x 96
+constexpr int kRegsSum = 104;
 constexpr int kLse = 4;            // query tiles whose lse is in shared memory
 constexpr int kRing = 4;           // units in flight
 constexpr int kPlanSms = 148;      // SMs the split is planned for (fixed: it sizes the workspace)
-constexpr int kPoly = 2;           // of eight pairs of exponentials, those on the FMA pipe
+constexpr int kPoly = 1;           // of eight pairs of exponentials, those on the FMA pipe
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
@@ -64,8 +70,8 @@ struct Cfg {
   static constexpr int kOffK = 0;               // two pairs of key tiles
   static constexpr int kOffQ = 4 * kTile;
   static constexpr int kOffLse = kOffQ + kQStages * kTile;
-  static constexpr int kOffMisc = kOffLse + kLse * 1024;
-  static constexpr int kSmem = kOffMisc + 1024 + 1024;  // + alignment slack
+  static constexpr int kOffMisc = kOffLse + kLse * 512;
+  static constexpr int kSmem = kOffMisc + 1024 + 2048 + 1024;  // barriers, half sums, alignment slack
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
 
@@ -75,10 +81,13 @@ struct Params {
   const float* score_in;  // nullable
   float* score_out;
   float* part;            // [Z][Bk * Hkv][C] when Z > 1
+  float* nl;              // [Bk * Hkv][all tiles][128]: -lse log2(e)
   int B, G, Hkv, T, Bk, n, C, causal;
   int GT, by_head;        // by_head: query tiles of one head
   int nb, rb;             // query tile: sequences x rows (box)
   int tiles;              // by_head: tiles of one head; else row tiles of a KV head (all n sequences)
+  int all;                // tiles of a KV head: n G heads' (by_head) or `tiles`
+  int N;                  // columns of the products: nb * rb rounded up to 16
   int Z, pairs;
   long long units;
   float scale_log2;
@@ -92,8 +101,20 @@ struct Unit {
   int i, g, r0;    // first tile: sequence of the group, query head of the KV head (by_head), row
   int r_min;       // by_head: first visible row of every head
   int z;
+  int pad[2];      // a multiple of 16 bytes: read as vectors
 };
 constexpr int kUnitInts = sizeof(Unit) / 4;
+static_assert(kUnitInts == 12, "");
+
+__device__ __forceinline__ void read_unit(Unit& x, const int* slot) {
+  int4* w = reinterpret_cast<int4*>(&x);
+#pragma unroll
+  for (int i = 0; i < kUnitInts / 4; ++i)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                 : "r"(smem_u32(slot + 4 * i))
+                 : "memory");
+}
 
 __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
   const long long t0 = clock64();
@@ -138,11 +159,11 @@ struct Tile {
       i += p.nb;
     }
   }
-  // valid columns
-  __device__ __forceinline__ int cols(const Params& p) const {
-    if (p.by_head) return min(128, p.T - r0);
-    if (p.GT >= 128) return min(128, p.GT - r0);
-    return min(p.nb, p.n - i) * p.GT;
+  // place among all tiles of the KV head
+  __device__ __forceinline__ int index(const Params& p) const {
+    if (p.by_head) return (i * p.G + g) * p.tiles + r0 / 128;
+    if (p.GT >= 128) return i * ((p.GT + 127) / 128) + r0 / 128;
+    return i / p.nb;
   }
 };
 
@@ -214,8 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sK = smem + C::kOffK;
   uint8_t* sQ = smem + C::kOffQ;
-  float* sLse = reinterpret_cast<float*>(smem + C::kOffLse);           // [kLse][128] log2 units
-  int* sLim = reinterpret_cast<int*>(smem + C::kOffLse + kLse * 512);  // [kLse][128] last visible key
+  float* sLse = reinterpret_cast<float*>(smem + C::kOffLse);  // [kLse][128] -lse in log2 units
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffMisc);
   uint64_t* k_full = bars + 0;    // [2] a pair of key tiles landed  (TMA)
   uint64_t* k_empty = bars + 2;   // [2] its last product done       (commit)
@@ -223,17 +243,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* q_empty = bars + 8;   // [kQ]
   uint64_t* s_full = bars + 12;   // [2 streams][2] S^T ready        (commit)
   uint64_t* s_empty = bars + 16;  // [2 streams][2] read             (4 warps)
-  uint64_t* l_full = bars + 20;   // [kLse] lse of a query tile      (lse warp)
-  uint64_t* l_empty = bars + 24;  // [kLse] read                     (8 warps)
+  uint64_t* l_full = bars + 20;   // [kLse] lse of a query tile      (bulk copy)
+  uint64_t* l_empty = bars + 24;  // [kLse] read                     (16 warps)
   uint64_t* u_full = bars + 28;   // [kRing] a unit published
-  uint64_t* u_empty = bars + 32;  // [kRing] read by loads, MMA issue, lse loads, 8 warps
+  uint64_t* u_empty = bars + 32;  // [kRing] read by loads, MMA issue, 16 warps
   uint64_t* drain = bars + 36;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc + 320);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* start_bk = reinterpret_cast<int*>(tmem_slot + 2);
   long long* start_off = reinterpret_cast<long long*>(smem + C::kOffMisc + 336);
   long long* red = start_off + 1;                                                  // [12]
-  volatile int* ring = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 512);  // [kRing][kUnitInts]
+  int* ring = reinterpret_cast<int*>(smem + C::kOffMisc + 768);  // [kRing][kUnitInts]
+  float* half_sum = reinterpret_cast<float*>(smem + C::kOffMisc + 1024);           // [parity][key tile][128]
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
@@ -247,15 +268,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 4);
+      mbar_init(&s_empty[i], 8);
     }
     for (int i = 0; i < kLse; ++i) {
       mbar_init(&l_full[i], 1);
-      mbar_init(&l_empty[i], 8);
+      mbar_init(&l_empty[i], 16);
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&u_full[i], 1);
-      mbar_init(&u_empty[i], 11);
+      mbar_init(&u_empty[i], 18);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -339,9 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         x.nt = -1;
         return;
       }
-      int* w = reinterpret_cast<int*>(&x);
-#pragma unroll
-      for (int i = 0; i < kUnitInts; ++i) w[i] = ring[slot * kUnitInts + i];
+      read_unit(x, ring + slot * kUnitInts);
       if (reads) mbar_arrive(&u_empty[slot]);
       ++nu;
     };
@@ -352,8 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto publish = [&](const Unit& x) -> bool {
           const int slot = nu % kRing;
           if (nu >= kRing && !mbar_sleep(&u_empty[slot], ((nu / kRing) - 1) & 1, abort_flag, p.status)) return false;
-          const int* w = reinterpret_cast<const int*>(&x);
-          for (int i = 0; i < kUnitInts; ++i) ring[slot * kUnitInts + i] = w[i];
+          *reinterpret_cast<Unit*>(ring + slot * kUnitInts) = x;
           mbar_arrive(&u_full[slot]);
           ++nu;
           return true;
@@ -416,9 +434,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++ku;
         Tile t = {x.i, x.g, x.r0};
         const uint32_t bytes = static_cast<uint32_t>(p.nb * p.rb) * 128 * C::kChunks;
+        const float* nl = p.nl + (static_cast<long long>(x.bk) * p.Hkv + x.hkv) * p.all * 128;
         for (int f = 0; f < x.nt; ++f, ++qt) {
           const int st = qt % kQ;
+          const int lt = qt % kLse;
           if (!(ok = mbar_sleep(&q_empty[st], ((qt / kQ) & 1) ^ 1, abort_flag, p.status))) break;
+          if (!(ok = mbar_sleep(&l_empty[lt], ((qt / kLse) & 1) ^ 1, abort_flag, p.status))) break;
+          mbar_arrive_expect_tx(&l_full[lt], 512);
+          bulk_load(sLse + 128 * lt, nl + static_cast<long long>(t.index(p)) * 128, 512, &l_full[lt]);
           mbar_arrive_expect_tx(&q_full[st], bytes);
 #pragma unroll
           for (int ch = 0; ch < C::kChunks; ++ch)
@@ -430,13 +453,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       // no bulk copy may still be writing shared memory when the CTA leaves
       for (int i = max(0, ku - 2); i < ku; ++i) mbar_drain(&k_full[i & 1], (i >> 1) & 1);
       for (int i = max(0, qt - kQ); i < qt; ++i) mbar_drain(&q_full[i % kQ], (i / kQ) & 1);
+      for (int i = max(0, qt - kLse); i < qt; ++i) mbar_drain(&l_full[i % kLse], (i / kLse) & 1);
     } else if (warp == 1) {
       // ---------------------------------------------------- MMA issue
       // The whole warp walks the tiles in step; one elected lane issues.  The
-      // lanes wait without a vote and agree on stopping once per tile.
+      // lanes wait without a vote and agree on stopping once per unit.
       const uint64_t dK0 = sdesc_sw128(smem_u32(sK), 16, 1024);
       const uint64_t dQ0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
       constexpr uint64_t kStep = C::kTile >> 4;
+      const uint32_t idesc = idesc_f16_f32(FP16, 128, p.N, 0, 0);
       int ku = 0, qt = 0;
       bool ok = true;
       while (ok) {
@@ -449,16 +474,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (nt == 0) continue;
         const int kb = ku & 1;
         ok = mbar_sleep(&k_full[kb], (ku >> 1) & 1, abort_flag, p.status);
-        Tile t = {x.i, x.g, x.r0};
         for (int f = 0; f < nt; ++f, ++qt) {
           const int st = qt % kQ, buf = qt & 1;
-          const uint32_t idesc =
-              idesc_f16_f32(FP16, 128, __shfl_sync(0xffffffffu, (t.cols(p) + 15) & ~15, 0), 0, 0);
           const uint32_t eh = ((qt >> 1) & 1) ^ 1, qh = (qt / kQ) & 1;
-          const bool r0 = mbar_try_wait(&s_empty[buf], eh), rq = mbar_try_wait(&q_full[st], qh);
+          // one look at all three barriers, whose latencies then overlap
+          const bool rq = mbar_try_wait(&q_full[st], qh), r0 = mbar_try_wait(&s_empty[buf], eh),
+                     r1 = mbar_try_wait(&s_empty[2 + buf], eh);
+          const uint64_t a = dK0 + 2 * kb * kStep, b = dQ0 + st * kStep;
           if (!rq) ok &= mbar_sleep(&q_full[st], qh, abort_flag, p.status);
           if (!r0) ok &= mbar_sleep(&s_empty[buf], eh, abort_flag, p.status);
-          const uint64_t a = dK0 + 2 * kb * kStep, b = dQ0 + st * kStep;
           __syncwarp();
           tc_fence_after();
           if (elect_one()) {
@@ -468,8 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           b + (kk >> 2) * 1024 + (kk & 3) * 2, idesc, kk ? 1u : 0u);
             tc_commit(&s_full[buf]);
           }
-          __syncwarp();
-          ok &= mbar_sleep(&s_empty[2 + buf], eh, abort_flag, p.status);
+          if (!r1) ok &= mbar_sleep(&s_empty[2 + buf], eh, abort_flag, p.status);
           __syncwarp();
           tc_fence_after();
           if (elect_one()) {
@@ -482,90 +505,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (f == nt - 1) tc_commit(&k_empty[kb]);
           }
           __syncwarp();
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          t.next(p, x);
         }
+        ok = __all_sync(0xffffffffu, ok);
         ++ku;
       }
       if (elect_one()) {
         tc_commit(drain);
         mbar_drain(drain, 0);
       }
-    } else if (warp == 2) {
-      // ---------------------------------------------------- lse and limits per column
-      int qt = 0;
-      bool ok = true;
-      while (ok) {
-        Unit x;
-        next_unit(x, false);
-        __syncwarp();
-        if (__any_sync(0xffffffffu, x.nt < 0)) break;
-        if (lane == 0) mbar_arrive(&u_empty[(nu - 1) % kRing]);
-        Tile t = {x.i, x.g, x.r0};
-        // this lane's values of a tile
-        float v[4];
-        int lim[4];
-        auto load = [&](const Tile& t) {
-          const int cols = t.cols(p);
-          const int b = x.bk * p.n + t.i;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c = lane + 32 * i;
-            v[i] = -INFINITY;
-            lim[i] = -1;
-            if (c < cols) {
-              long long at;
-              int tok;
-              if (p.by_head) {
-                tok = t.r0 + c;
-                at = (static_cast<long long>(b) * p.Hkv * p.G + x.hkv * p.G + t.g) * p.T + tok;
-              } else if (p.GT >= 128) {
-                tok = (t.r0 + c) % p.T;
-                at = (static_cast<long long>(b) * p.Hkv + x.hkv) * p.GT + t.r0 + c;
-              } else {
-                const int i2 = c / p.GT, r = c - i2 * p.GT;
-                tok = r % p.T;
-                at = (static_cast<long long>(b + i2) * p.Hkv + x.hkv) * p.GT + r;
-              }
-              v[i] = __ldg(p.lse + at);
-              lim[i] = p.causal ? x.len - p.T + tok : INT_MAX;
-            }
-          }
-        };
-        if (x.nt > 0) load(t);
-        for (int f = 0; f < x.nt; ++f, ++qt) {
-          float nl[4];
-          int lm[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // a query that saw nothing (lse -inf) adds nothing
-            nl[i] = v[i] == -INFINITY ? -INFINITY : -v[i] * kLog2e;
-            lm[i] = lim[i];
-          }
-          if (f + 1 < x.nt) {
-            t.next(p, x);
-            load(t);  // on its way while this one is handed over
-          }
-          const int st = qt % kLse;
-          ok = __all_sync(0xffffffffu, mbar_sleep(&l_empty[st], ((qt / kLse) & 1) ^ 1, abort_flag, p.status));
-          if (!ok) break;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            sLse[128 * st + lane + 32 * i] = nl[i];
-            sLim[128 * st + lane + 32 * i] = lm[i];
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&l_full[st]);
-        }
-      }
     }
     __syncwarp();
   } else {
     reg_alloc<kRegsSum>();
     // -------------------------------------------------------- sums per key
-    const int s = (warp >> 2) - 1;
+    const int s = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1;  // key tile, columns [64 half, 64 half + 64)
     const int row = (warp & 3) * 32 + lane;
-    const uint32_t s_addr = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256 * s;
+    const uint32_t s_addr = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256 * s + 64 * half;
+    const int lim = p.by_head ? p.T : (p.GT >= 128 ? p.GT : p.n * p.GT);
+    const int step = p.nb * p.rb;
     int nu = 0, qt = 0;
     bool ok = true;
     while (ok) {
@@ -573,67 +530,62 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, mbar_sleep(&u_full[slot], (nu / kRing) & 1, abort_flag, p.status));
       if (!ok) break;
       Unit x;
-      {
-        int* w = reinterpret_cast<int*>(&x);
-#pragma unroll
-        for (int i = 0; i < kUnitInts; ++i) w[i] = ring[slot * kUnitInts + i];
-      }
+      read_unit(x, ring + slot * kUnitInts);
       __syncwarp();
       if (lane == 0) mbar_arrive(&u_empty[slot]);
       ++nu;
       if (x.nt < 0) break;
       const int tile0 = x.key0 + 128 * s, key = tile0 + row;
       const long long at = static_cast<long long>(x.bk * p.Hkv + x.hkv) * p.C + key;
-      const float before = p.Z == 1 && p.score_in && key < x.len ? p.score_in[at] : 0.f;
+      const float before = p.Z == 1 && !half && p.score_in && key < x.len ? p.score_in[at] : 0.f;
       float acc = 0.f, comp = 0.f;
-      Tile t = {x.i, x.g, x.r0};
+      // rows r, r + step, .. below lim, from r_min again for every head
+      int r = p.by_head || p.GT >= 128 ? x.r0 : x.i * p.GT;
+      // first row whose token sees every key of this tile
+      const int r_open = !p.causal ? INT_MIN : tile0 + 127 - (x.len - p.T);
+#pragma unroll 1
       for (int f = 0; f < x.nt; ++f, ++qt) {
         const int buf = qt & 1, st = qt % kLse;
-        const int cols = t.cols(p);
-        const bool mask = p.causal && tile0 + 127 > x.len - p.T + (p.by_head ? t.r0 : 0);
+        const int cols = min(step, lim - r);
+        const bool mask = (p.by_head ? r : 0) < r_open;
         const uint32_t lh = (qt / kLse) & 1, sh = (qt >> 1) & 1;
         const bool lr = mbar_try_wait(&l_full[st], lh), sr = mbar_try_wait(&s_full[2 * s + buf], sh);
         ok = lr || mbar_sleep(&l_full[st], lh, abort_flag, p.status);
         ok &= sr || mbar_sleep(&s_full[2 * s + buf], sh, abort_flag, p.status);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
-        const float* nl = sLse + 128 * st;
-        const int* lm = sLim + 128 * st;
+        const float* nl = sLse + 128 * st + 64 * half;
         const uint32_t src = s_addr + 128 * buf;
         float a[4] = {0.f, 0.f, 0.f, 0.f};
         if (!mask && cols == 128) {
-          // 32 columns at a time, the next 32 on their way
           float va[32], vb[32];
           tmem_ld32(src, va);
           tc_wait_ld();
-          tmem_ld32(src + 32, vb);
+          tmem_ld32(src + 32, vb);  // on its way meanwhile
           sum32(va, nl, p.scale_log2, a);
-          tc_wait_ld();
-          tmem_ld32(src + 64, va);
-          sum32(vb, nl + 32, p.scale_log2, a);
-          tc_wait_ld();
-          tmem_ld32(src + 96, vb);
-          sum32(va, nl + 64, p.scale_log2, a);
           tc_wait_ld();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&s_empty[2 * s + buf]);
-          sum32(vb, nl + 96, p.scale_log2, a);
+          sum32(vb, nl + 32, p.scale_log2, a);
           __syncwarp();
           if (lane == 0) mbar_arrive(&l_empty[st]);
         } else {
-          const int chunks = (cols + 31) >> 5;
+          const int chunks = (min(cols - 64 * half, 64) + 31) >> 5;
 #pragma unroll 1
           for (int c = 0; c < chunks; ++c) {
+            // last key that the query of column 64 half + 32 c + lane sees;
+            // none where there is no query (its column holds anything)
+            const int col = 64 * half + 32 * c + lane;
+            int last = -1;
+            if (col < cols) last = !mask ? INT_MAX : x.len - p.T + (p.by_head ? r + col : (r + col) % p.T);
             float v[32];
             tmem_ld32(src + 32 * c, v);
             tc_wait_ld();
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const int col = 32 * c + i;
-              const float e = ex2_approx(fmaf(v[i], p.scale_log2, nl[col]));
-              // a column that is no query of this tile has the limit -1
-              if (key <= lm[col]) a[i & 3] += e;
+              const float e = ex2_approx(fmaf(v[i], p.scale_log2, nl[32 * c + i]));
+              if (key <= __shfl_sync(0xffffffffu, last, i)) a[i & 3] += e;
             }
           }
           tc_fence_before();
@@ -648,10 +600,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float z = acc + y;
         comp = (z - acc) - y;
         acc = z;
-        t.next(p, x);
+        r += step;
+        if (r >= lim) r = x.r_min;
       }
       if (!ok) break;
-      if (key < p.C) {
+      // the halves join
+      float* hs = half_sum + 256 * (nu & 1) + 128 * s;
+      if (half) hs[row] = acc;
+      named_barrier_sync(1 + 4 * s + (warp & 3), 64);
+      if (!half) acc += hs[row];
+      if (!half && key < p.C) {
         if (p.Z > 1) {
           p.part[static_cast<long long>(x.z) * p.Bk * p.Hkv * p.C + at] = acc;
         } else {
@@ -663,10 +621,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!p.by_head && p.Z == 1) {
       const int tid = threadIdx.x - 128;
       const long long tail = static_cast<long long>(p.Bk) * p.Hkv * p.pairs;
-      for (long long u = blockIdx.x; u < tail; u += gridDim.x) {
+      for (long long u = 2LL * blockIdx.x + (tid >> 8); u < tail; u += 2LL * gridDim.x) {
         const int bh = static_cast<int>(u / p.pairs), key = static_cast<int>(u - static_cast<long long>(bh) * p.pairs) * 256;
-        if (key >= clamped_len(p, bh / p.Hkv) && key + tid < p.C)
-          p.score_out[static_cast<long long>(bh) * p.C + key + tid] = 0.f;
+        if (key >= clamped_len(p, bh / p.Hkv) && key + (tid & 255) < p.C)
+          p.score_out[static_cast<long long>(bh) * p.C + key + (tid & 255)] = 0.f;
       }
     }
   }
@@ -803,6 +761,39 @@ __global__ void __launch_bounds__(kStreamThreads, NT == 4 ? 1 : 2)
   for (int key = done + threadIdx.x; key < end; key += kStreamThreads) p.score_out[base + key] = 0.f;
 }
 
+// -lse log2(e) in the order of the query tiles, two tiles per block.
+__global__ void __launch_bounds__(256) lse_kernel(const Params p) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const long long tile = blockIdx.x * 2LL + (threadIdx.x >> 7);
+  const int c = threadIdx.x & 127;
+  if (tile >= static_cast<long long>(p.Bk) * p.Hkv * p.all) return;
+  const int bh = static_cast<int>(tile / p.all), f = static_cast<int>(tile - static_cast<long long>(bh) * p.all);
+  const int bk = bh / p.Hkv, hkv = bh - bk * p.Hkv;
+  float l = -INFINITY;
+  if (p.by_head) {
+    const int o = f / p.tiles, i = o / p.G, tok = 128 * (f - o * p.tiles) + c;
+    if (tok < p.T)
+      l = __ldg(p.lse + (static_cast<long long>(bk * p.n + i) * p.Hkv * p.G + hkv * p.G + o - i * p.G) * p.T + tok);
+  } else {
+    int i, r;
+    bool in;
+    if (p.GT >= 128) {
+      const int of = (p.GT + 127) / 128;
+      i = f / of;
+      r = 128 * (f - i * of) + c;
+      in = r < p.GT;
+    } else {
+      i = f * p.nb + c / p.GT;
+      r = c % p.GT;
+      in = c < p.nb * p.GT && i < p.n;
+    }
+    if (in) l = __ldg(p.lse + (static_cast<long long>(bk * p.n + i) * p.Hkv + hkv) * p.GT + r);
+  }
+  // a query that saw nothing (lse -inf) adds nothing
+  p.nl[tile * 128 + c] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+}
+
 // score_out = score_in + the parts of a split unit, in order.
 __global__ void __launch_bounds__(256) weight_sum_kernel(const Params p) {
   grid_dep_launch();
@@ -847,6 +838,8 @@ bool make_plan(Params& p, int B, int G, int Hkv, int T, int Bk, int C) {
   }
   if (tiles > INT_MAX) return false;
   if (!p.by_head) p.tiles = static_cast<int>(tiles);
+  p.all = static_cast<int>(tiles);
+  p.N = (p.nb * p.rb + 15) & ~15;
   p.pairs = (C + 255) / 256;
   const long long units = static_cast<long long>(Bk) * Hkv * p.pairs;
   // two units per SM, of at least four query tiles each, 16 parts at most
@@ -855,7 +848,7 @@ bool make_plan(Params& p, int B, int G, int Hkv, int T, int Bk, int C) {
   if (z > 16) z = 16;
   p.Z = z < 1 ? 1 : static_cast<int>(z);
   p.units = units * p.Z;
-  return units <= INT_MAX;
+  return units <= INT_MAX && static_cast<long long>(Bk) * Hkv * tiles <= INT_MAX;
 }
 
 template <int D, bool FP16>
@@ -863,11 +856,17 @@ cudaError_t run(const Params& p, const CUtensorMap& mq, const CUtensorMap& mk, i
   cudaError_t e = cudaFuncSetAttribute(weight_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
+  const long long tiles = static_cast<long long>(p.Bk) * p.Hkv * p.all;
+  e = launch_chained(lse_kernel, dim3(static_cast<unsigned>((tiles + 1) / 2)), dim3(256), 0, st, p);
+  if (e != cudaSuccess) return e;
   e = launch_chained(weight_kernel<D, FP16>, dim3(grid), dim3(kThreads), Cfg<D>::kSmem, st, mq, mk, p);
   if (e != cudaSuccess || p.Z == 1) return e;
   const long long n = static_cast<long long>(p.Bk) * p.Hkv * p.C;
   return launch_chained(weight_sum_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, st, p);
 }
+
+size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
+size_t lse_bytes(const Params& p) { return static_cast<size_t>(p.Bk) * p.Hkv * p.all * 512; }
 
 bool streams(const Params& p) { return static_cast<long long>(p.n) * p.GT <= kStreamRows; }
 
@@ -893,8 +892,8 @@ cudaError_t run_stream(const WeightLaunch& a, const Params& p, cudaStream_t st) 
 size_t weight_workspace_bytes(int B, int G, int Hkv, int T, int Bk, int C) {
   Params p = {};
   if (!make_plan(p, B, G, Hkv, T, Bk, C)) return 0;
-  const size_t part = p.Z > 1 && !streams(p) ? static_cast<size_t>(p.Z) * Bk * Hkv * C * 4 : 0;
-  return 256 + ((part + 255) & ~static_cast<size_t>(255));
+  if (streams(p)) return 256;
+  return 256 + align256(lse_bytes(p)) + align256(p.Z > 1 ? static_cast<size_t>(p.Z) * Bk * Hkv * C * 4 : 0);
 }
 
 cudaError_t launch_weight(const WeightLaunch& a, cudaStream_t st) {
@@ -907,7 +906,8 @@ cudaError_t launch_weight(const WeightLaunch& a, cudaStream_t st) {
   p.causal = a.causal;
   p.scale_log2 = kLog2e / (a.d == 128 ? 11.313708498984761f : 8.0f);
   p.status = reinterpret_cast<int*>(a.ws);
-  p.part = reinterpret_cast<float*>(a.ws + 256);
+  p.nl = reinterpret_cast<float*>(a.ws + 256);
+  p.part = reinterpret_cast<float*>(a.ws + 256 + align256(lse_bytes(p)));
   if (streams(p)) {
     if (a.d == 128) return a.fp16 ? run_stream<128, true>(a, p, st) : run_stream<128, false>(a, p, st);
     return a.fp16 ? run_stream<64, true>(a, p, st) : run_stream<64, false>(a, p, st);
