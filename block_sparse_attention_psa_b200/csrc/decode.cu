@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   long long* red = start_off + 2;                                                 // [20]
   volatile int* ring = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 512); // [kRing][kPieceInts]
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dV0 = sdesc_sw128(smem_u32(sV), D == 128 ? 16384 : 0, 1024);
       constexpr uint64_t kStep = C::kTile >> 4;
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, mbar_sleep(bar, parity, abort_flag, p.status));
+        return mbar_sleep_warp(bar, parity, abort_flag, p.status);
       };
       int np = 0, cnt = 0;         // pieces read, items issued
       int t = 0;                   // running key tile
@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int np = 0, ns = 0, no = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_sleep(bar, parity, abort_flag, p.status));
+      return mbar_sleep_warp(bar, parity, abort_flag, p.status);
     };
     while (ok) {
       const int slot = np % kRing;
@@ -562,10 +562,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       {
         int* w = reinterpret_cast<int*>(&c);
 #pragma unroll
-        for (int i = 0; i < kPieceInts; ++i) w[i] = ring[slot * kPieceInts + i];
+        for (int i = 0; i < kPieceInts; ++i) w[i] = uniform(ring[slot * kPieceInts + i]);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&pc_empty[slot]);
+      __syncwarp();
       ++np;
       if (c.nt == 0) break;
       const int sub = s ^ (c.items & 1);
@@ -617,6 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int o = x * 16; o < bytes; o += 128 * 16) st_shared_v4(base + o, 0u, 0u, 0u, 0u);
           }
           fence_async_shared();
+          __syncwarp();
         }
         if (any_valid) {
           tc_fence_after();
@@ -670,6 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (h == 0) {
               __syncwarp();
               if (lane == 0) mbar_arrive(&p_full[2 * s]);
+              __syncwarp();
             }
           }
           l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
@@ -678,6 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[2 * s + 1]);
+        __syncwarp();
       }
       if (!ok) break;
       // the piece's part
@@ -732,7 +736,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p, ui
   grid_dep_launch();
   grid_dep_wait();
   const int row = blockIdx.x;  // (b, hkv, r)
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int bh = row / p.GT, r = row - bh * p.GT;
   const int b = bh / p.Hkv, hkv = bh - b * p.Hkv;
   // where the row's parts are: first CTA, count and place of the first

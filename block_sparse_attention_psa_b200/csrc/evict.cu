@@ -46,7 +46,7 @@ struct SelectParams {
   int* status;
   int B, Hkv, C, budget, sink, recent;
   int slice;             // slots per CTA, a multiple of 32 * warps
-  int keys_on_chip;
+  int keys_on_chip, pos_on_chip;
 };
 
 // Order-preserving key of a score: NaN as the lowest (-inf), -0 as +0.
@@ -59,10 +59,11 @@ __device__ __forceinline__ uint32_t score_key(float f) {
 // Exclusive prefix over the block's warps of two warp-uniform counts, and the
 // block's totals.  `buf` holds 33 pairs.
 __device__ __forceinline__ int2 warps_exclusive(int2* buf, int2 mine, int2& total) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   __syncthreads();
   if (lane == 0) buf[warp] = mine;
   __syncthreads();
+  __syncwarp();
   // every warp scans for itself: no third barrier
   int2 v = lane < warps ? buf[lane] : make_int2(0, 0), s = v;
 #pragma unroll
@@ -80,6 +81,7 @@ __device__ __forceinline__ int2 warps_exclusive(int2* buf, int2 mine, int2& tota
 // Shared by the cluster's CTAs (each reads the others').
 struct SelectShared {
   uint32_t hist[3][kBins];  // one per round: nothing is cleared while it may still be read
+  uint32_t coarse[3][32];   // sums of 64 bins
   int2 count[2];            // totals of a CTA, one per exchange
   int last;                 // latest position
 };
@@ -91,7 +93,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1) select_kernel(const SelectPara
   extern __shared__ __align__(16) uint32_t smem[];
   __shared__ __align__(16) SelectShared sh;
   __shared__ int2 buf[33];
-  __shared__ uint32_t wsum[32];
   __shared__ uint32_t pick[3];  // chosen bin, keys above it, keys in it
   cg::cluster_group cl = cg::this_cluster();
   const int rank = CL ? static_cast<int>(cl.block_rank()) : 0;
@@ -106,15 +107,17 @@ __global__ void __launch_bounds__(kMaxThreads, 1) select_kernel(const SelectPara
   auto peer = [&](int r) -> const SelectShared* { return CL ? cl.map_shared_rank(&sh, r) : &sh; };
   const int bh = blockIdx.x / ncta;
   const int b = bh / p.Hkv;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x;
-  uint32_t* stay = smem;                      // one bit per slot of the slice
-  uint32_t* keys = smem + (p.slice >> 5);     // the slice's keys (when they fit)
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5), nthr = blockDim.x;
+  const int words = p.slice >> 5;
+  uint32_t* stay = smem;                                  // one bit per slot of the slice
+  int2* rank_at = reinterpret_cast<int2*>(smem + words);  // holes and late survivors before each word
+  uint32_t* keys = smem + 3 * words;                      // the slice's keys (when they fit), 0 past its end
   for (int i = tid; i < 3 * kBins / 4; i += nthr) reinterpret_cast<uint4*>(&sh.hist[0][0])[i] = make_uint4(0, 0, 0, 0);
   grid_dep_launch();
   grid_dep_wait();
 
   int len = p.cache_len ? __ldg(p.cache_len + b) : p.C;
-  len = min(max(len, 0), p.C);
+  len = uniform(min(max(len, 0), p.C));
   if (blockIdx.x == 0) {
     // one writer of the status word: the lengths of all sequences
     bool bad = false;
@@ -139,20 +142,36 @@ __global__ void __launch_bounds__(kMaxThreads, 1) select_kernel(const SelectPara
     return;
   }
 
-  // ---- the latest position of the head
+  // ---- keys, and the latest position of the head
   const int s0 = rank * p.slice, s1 = min(s0 + p.slice, len);
+  const bool guarded = pos && p.recent > 0;
   int last = len - 1;
-  if (pos && p.recent > 0) {
+  int* spos = reinterpret_cast<int*>(keys + p.slice);  // positions next to the keys (pos_on_chip)
+  if (guarded) {
     last = INT_MIN;
+    if (p.pos_on_chip) {
 #pragma unroll 8
-    for (int i = s0 + tid; i < s1; i += nthr) last = max(last, __ldg(pos + i));
+      for (int i = s0 + tid; i < s1; i += nthr) {
+        const int at = __ldg(pos + i);
+        const float f = __ldg(score + i);
+        spos[i - s0] = at;
+        keys[i - s0] = score_key(f);
+        last = max(last, at);
+      }
+    } else {
+#pragma unroll 8
+      for (int i = s0 + tid; i < s1; i += nthr) last = max(last, __ldg(pos + i));
+    }
+    __syncwarp();
     last = __reduce_max_sync(0xffffffffu, last);
     if (lane == 0) buf[warp].x = last;
     __syncthreads();
+    __syncwarp();
     last = __reduce_max_sync(0xffffffffu, lane < (nthr >> 5) ? buf[lane].x : INT_MIN);
     if constexpr (CL) {
       if (tid == 0) sh.last = last;
       cl.sync();
+      __syncwarp();
       last = __reduce_max_sync(0xffffffffu, lane < ncta ? peer(lane)->last : INT_MIN);
     }
   }
@@ -164,76 +183,119 @@ __global__ void __launch_bounds__(kMaxThreads, 1) select_kernel(const SelectPara
     const uint32_t k = score_key(__ldg(score + i));
     return at < p.sink || at > guard ? 0xffffffffu : k;
   };
-  if (p.keys_on_chip) {
+  if (guarded && p.pos_on_chip) {
+    for (int i = tid; i < s1 - s0; i += nthr)
+      if (spos[i] < p.sink || spos[i] > guard) keys[i] = 0xffffffffu;
+  } else if (p.keys_on_chip) {
 #pragma unroll 8
     for (int i = s0 + tid; i < s1; i += nthr) keys[i - s0] = make_key(i);
   }
-  auto key = [&](int i) -> uint32_t { return p.keys_on_chip ? keys[i - s0] : make_key(i); };
+  // (no entry has key 0: the lowest score, -inf, has 0x007fffff)
+  if (p.keys_on_chip)
+    for (int i = max(s1 - s0, 0) + tid; i < p.slice; i += nthr) keys[i] = 0u;
+  auto key = [&](int i) -> uint32_t { return p.keys_on_chip ? keys[i - s0] : (i < s1 ? make_key(i) : 0u); };
   __syncthreads();
 
   // ---- radix select of the nk-th largest key
+  // After a round whose bin is needed whole, the bits so far decide.
   uint32_t prefix = 0, need = static_cast<uint32_t>(nk), equal = 0;
+  int shift = 0;
 #pragma unroll 1
-  for (int round = 0; round < 3; ++round) {
-    const int shift = round == 0 ? 21 : (round == 1 ? 10 : 0);
+  for (int round = 0; round < 3 && need != equal; ++round) {
+    shift = round == 0 ? 21 : (round == 1 ? 10 : 0);
     const int bits = round == 2 ? 10 : 11;
     const uint32_t mask = (1u << bits) - 1u;
     uint32_t* hist = sh.hist[round];
-    const int trips = (s1 - s0 + nthr - 1) / nthr;
-    for (int it = 0; it < trips; ++it) {
-      const int i = s0 + it * nthr + tid;
-      uint32_t bin = 0xffffffffu;
-      if (i < s1) {
-        const uint32_t k = key(i);
-        if (round == 0 || (k >> (shift + bits)) == prefix) bin = (k >> shift) & mask;
+    // four keys per thread and step
+#pragma unroll 2
+    for (int it = tid; it < p.slice / 4; it += nthr) {
+      uint32_t k[4];
+      if (p.keys_on_chip) {
+        const uint4 q = reinterpret_cast<const uint4*>(keys)[it];
+        k[0] = q.x, k[1] = q.y, k[2] = q.z, k[3] = q.w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) k[j] = key(s0 + 4 * it + j);
+      }
+      bool in[4], one = true;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        in[j] = k[j] != 0u && (round == 0 || (k[j] >> (shift + bits)) == prefix);
+        k[j] = (k[j] >> shift) & mask;
+        one = one && in[j] && k[j] == k[0];
       }
       // a warp whose keys share one bin (equal scores) adds once
-      int same;
-      __match_all_sync(0xffffffffu, bin, &same);
-      if (same) {
-        if (lane == 0 && bin != 0xffffffffu) atomicAdd(&hist[bin], 32u);
-      } else if (bin != 0xffffffffu) {
-        atomicAdd(&hist[bin], 1u);
+      const uint32_t lead = static_cast<uint32_t>(uniform(k[0]));  // (all lanes take part)
+      one = one && k[0] == lead;
+      if (__all_sync(0xffffffffu, one)) {
+        if (lane == 0) atomicAdd(&hist[k[0]], 128u);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (in[j]) atomicAdd(&hist[k[j]], 1u);
       }
+    }
+    __syncthreads();
+    for (int c = warp; c < 32; c += nthr >> 5) {
+      const uint2 h = reinterpret_cast<const uint2*>(hist)[32 * c + lane];
+      __syncwarp();
+      const uint32_t n = __reduce_add_sync(0xffffffffu, h.x + h.y);
+      if (lane == 0) sh.coarse[round][c] = n;
+      __syncwarp();
     }
     sync_all();
-    // thread t has the bins [kBins - per (t + 1), kBins - per t): counts above
-    // them by a scan, and the bin where the count passes `need`
-    const int per = kBins / nthr;
-    const int low = kBins - per * (tid + 1);
-    uint32_t mine = 0;
-    for (int j = 0; j < per; ++j)
-      for (int r = 0; r < ncta; ++r) mine += peer(r)->hist[round][low + j];
-    uint32_t inc = mine;
+    __syncwarp();
+    if (warp == 0) {
+      // the group of 64 bins in which the count from the top passes `need`,
+      // then the bin: two reads of every CTA, a few words each
+      uint32_t n = 0, above = 0;
+      int c = 31 - lane;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += u;
-    }
-    if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    uint32_t at = inc - mine;
-    for (int w = 0; w < warp; ++w) at += wsum[w];
-    if (at < need && need <= at + mine) {
-      for (int j = per - 1; j >= 0; --j) {
-        uint32_t n = 0;
-        for (int r = 0; r < ncta; ++r) n += peer(r)->hist[round][low + j];
-        if (at + n >= need) {
-          pick[0] = static_cast<uint32_t>(low + j);
-          pick[1] = at;
-          pick[2] = n;
-          break;
+      for (int r = 0; r < (CL ? 8 : 1); ++r)
+        if (r < ncta) n += peer(r)->coarse[round][c];
+      uint32_t inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+      }
+      int owner = __ffs(__ballot_sync(0xffffffffu, inc >= need)) - 1;
+      above = __shfl_sync(0xffffffffu, inc - n, owner);
+      c = __shfl_sync(0xffffffffu, c, owner);
+      // lane l: the bins 64 c + 63 - 2 l (first) and the one below it
+      uint32_t hi = 0, lo = 0;
+#pragma unroll
+      for (int r = 0; r < (CL ? 8 : 1); ++r)
+        if (r < ncta) {
+          const uint2 h = reinterpret_cast<const uint2*>(peer(r)->hist[round])[32 * c + 31 - lane];
+          hi += h.y;
+          lo += h.x;
         }
-        at += n;
+      n = hi + lo;
+      inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+      }
+      owner = __ffs(__ballot_sync(0xffffffffu, above + inc >= need)) - 1;
+      if (lane == owner) {
+        above += inc - n;
+        const bool first = above + hi >= need;
+        pick[0] = static_cast<uint32_t>(64 * c + 63 - 2 * lane - (first ? 0 : 1));
+        pick[1] = first ? above : above + hi;
+        pick[2] = first ? hi : lo;
       }
     }
     __syncthreads();
-    prefix = (prefix << bits) | pick[0];
-    need -= pick[1];
-    equal = pick[2];
-    // (the next round's barrier keeps `pick` and `wsum` until all have read)
+    __syncwarp();
+    prefix = (prefix << bits) | static_cast<uint32_t>(uniform(pick[0]));
+    need -= static_cast<uint32_t>(uniform(pick[1]));
+    equal = static_cast<uint32_t>(uniform(pick[2]));
+    // (the next round's barriers keep `pick` until all have read)
   }
-  // prefix is K*; of the `equal` entries with that key the first `need` stay
+  // prefix is K* (its bits from `shift` on); of the `equal` entries with them
+  // the first `need` stay
 
   // ---- which entries stay; each warp owns the slots [w0, w1)
   const int per_warp = p.slice / (nthr >> 5);
@@ -242,53 +304,91 @@ __global__ void __launch_bounds__(kMaxThreads, 1) select_kernel(const SelectPara
   int eq_at = 0;
   if (need < equal) {  // the same everywhere: ties are cut, so they are ranked
     int eq = 0;
-    for (int i = w0 + lane; i - lane < w1; i += 32)
-      eq += __popc(__ballot_sync(0xffffffffu, i < w1 && key(i) == prefix));
+    for (int i = w0 + lane; i - lane < w1; i += 32) {
+      const bool tie = i < w1 && key(i) >> shift == prefix;
+      __syncwarp();
+      eq += __popc(__ballot_sync(0xffffffffu, tie));
+    }
+    __syncwarp();
     eq_at = warps_exclusive(buf, make_int2(eq, 0), total).x;
     if constexpr (CL) {
       if (tid == 0) sh.count[0] = total;
       cl.sync();
+      __syncwarp();
       for (int r = 0; r < rank; ++r) eq_at += peer(r)->count[0].x;
     }
   }
-  int2 n = make_int2(0, 0);  // holes, late survivors
-  for (int i = w0 + lane; i - lane < w1; i += 32) {
-    const uint32_t k = i < w1 ? key(i) : 0u;
-    const uint32_t tie = __ballot_sync(0xffffffffu, i < w1 && k == prefix);
-    const int before = eq_at + __popc(tie & ((1u << lane) - 1u));
-    const bool in = i < w1 && (k > prefix || (k == prefix && (need == equal || before < static_cast<int>(need))));
-    eq_at += __popc(tie);
+  // slots of a word (32 from i0 on) below x
+  auto below = [](int x, int i0) -> uint32_t {
+    return x >= i0 + 32 ? 0xffffffffu : (x <= i0 ? 0u : (1u << (x - i0)) - 1u);
+  };
+  const bool cut = need < equal;
+#pragma unroll 2
+  for (int i0 = w0; i0 < w1; i0 += 32) {
+    const uint32_t k = key(i0 + lane) >> shift;
+    bool in = k >= prefix;
+    if (cut) {
+      const uint32_t tie = __ballot_sync(0xffffffffu, k == prefix);
+      in = in && (k > prefix || eq_at + __popc(tie & ((1u << lane) - 1u)) < static_cast<int>(need));
+      eq_at += __popc(tie);
+    }
     const uint32_t word = __ballot_sync(0xffffffffu, in);
-    if (lane == 0) stay[(i - s0) >> 5] = word;
-    n.x += __popc(__ballot_sync(0xffffffffu, i < w1 && i < nk && !in));
-    n.y += __popc(__ballot_sync(0xffffffffu, in && i >= nk));
+    if (lane == 0) stay[(i0 - s0) >> 5] = word;
   }
-  int2 base = warps_exclusive(buf, n, total);
+  // ranks of the holes and of the late survivors, a word per thread
+  int2 base = make_int2(0, 0);
+  const int have = (max(s1 - s0, 0) + 31) >> 5;
+  for (int w = 0; w < have; w += nthr) {
+    int2 n = make_int2(0, 0), total;
+    if (w == 0) __syncthreads();  // all of stay[] is there
+    if (w + tid < have) {
+      const uint32_t word = stay[w + tid], all = below(s1, s0 + 32 * (w + tid)), early = below(nk, s0 + 32 * (w + tid));
+      n.x = __popc(all & early & ~word);
+      n.y = __popc(word & ~early);
+    }
+    int2 inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int ux = __shfl_up_sync(0xffffffffu, inc.x, o), uy = __shfl_up_sync(0xffffffffu, inc.y, o);
+      if (lane >= o) {
+        inc.x += ux;
+        inc.y += uy;
+      }
+    }
+    const int2 warp_total =
+        make_int2(__shfl_sync(0xffffffffu, inc.x, 31), __shfl_sync(0xffffffffu, inc.y, 31));
+    const int2 before = warps_exclusive(buf, warp_total, total);
+    if (w + tid < have)
+      rank_at[w + tid] = make_int2(base.x + before.x + inc.x - n.x, base.y + before.y + inc.y - n.y);
+    base.x += total.x;
+    base.y += total.y;
+  }
+  int2 first = make_int2(0, 0);
   if constexpr (CL) {
-    if (tid == 0) sh.count[1] = total;
+    if (tid == 0) sh.count[1] = base;
     cl.sync();
     for (int r = 0; r < rank; ++r) {
       const int2 c = peer(r)->count[1];
-      base.x += c.x;
-      base.y += c.y;
+      first.x += c.x;
+      first.y += c.y;
     }
+  } else {
+    __syncthreads();
   }
-  __syncwarp();
-  int at = base.y;
-  for (int i = w0 + lane; i - lane < w1; i += 32) {
-    const bool in = (stay[(i - s0) >> 5] >> lane) & 1u;
-    const uint32_t far = __ballot_sync(0xffffffffu, in && i >= nk);
-    if (in && i >= nk) late[at + __popc(far & ((1u << lane) - 1u))] = i;
-    at += __popc(far);
-    if (in && i < nk) kept[i] = i;
+#pragma unroll 2
+  for (int i0 = w0; i0 < w1; i0 += 32) {
+    const int w = (i0 - s0) >> 5;
+    const uint32_t word = stay[w], early = below(nk, i0), bit = 1u << lane;
+    const uint32_t far = word & ~early;
+    if (far & bit) late[first.y + rank_at[w].y + __popc(far & (bit - 1u))] = i0 + lane;
+    if (word & early & bit) kept[i0 + lane] = i0 + lane;
   }
   sync_all();  // orders the list's global writes; nobody reads another's shared memory after it
-  at = base.x;
-  for (int i = w0 + lane; i - lane < min(w1, nk); i += 32) {
-    const bool hole = i < w1 && i < nk && !((stay[(i - s0) >> 5] >> lane) & 1u);
-    const uint32_t open = __ballot_sync(0xffffffffu, hole);
-    if (hole) kept[i] = *(volatile int*)(late + at + __popc(open & ((1u << lane) - 1u)));
-    at += __popc(open);
+#pragma unroll 4
+  for (int i0 = w0; i0 < min(w1, nk); i0 += 32) {
+    const int w = (i0 - s0) >> 5;
+    const uint32_t open = below(min(nk, w1), i0) & ~stay[w], bit = 1u << lane;
+    if (open & bit) kept[i0 + lane] = __ldcg(late + first.x + rank_at[w].x + __popc(open & (bit - 1u)));
   }
 }
 
@@ -385,9 +485,11 @@ cudaError_t launch_evict(const EvictLaunch& a, cudaStream_t st) {
   // four slots or more per thread; two CTAs per SM when there are more heads than SMs
   int threads = heads * ncta > 148 ? kMaxThreads / 2 : kMaxThreads;
   while (threads > 128 && threads * 4 > part) threads /= 2;
-  s.slice = (part + threads - 1) / threads * threads;
+  s.slice = (part + 4 * threads - 1) / (4 * threads) * 4 * threads;
   s.keys_on_chip = s.slice <= kSmemKeys;
-  const size_t smem = static_cast<size_t>(s.slice / 32 + (s.keys_on_chip ? s.slice : 0)) * 4;
+  s.pos_on_chip = 2 * s.slice <= kSmemKeys;
+  const size_t smem =
+      static_cast<size_t>(3 * (s.slice / 32) + (s.keys_on_chip ? s.slice : 0) + (s.pos_on_chip ? s.slice : 0)) * 4;
   auto kernel = ncta > 1 ? select_kernel<true> : select_kernel<false>;
   cudaError_t e = cudaSuccess;
   if (smem > 20 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 180 * 1024);

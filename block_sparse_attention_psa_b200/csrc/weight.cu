@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* ring = reinterpret_cast<int*>(smem + C::kOffMisc + 768);  // [kRing][kUnitInts]
   float* half_sum = reinterpret_cast<float*>(smem + C::kOffMisc + 1024);           // [parity][key tile][128]
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 1);
@@ -471,6 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nt = __shfl_sync(0xffffffffu, x.nt, 0);
         if (nt < 0) break;
         if (elect_one()) mbar_arrive(&u_empty[(nu - 1) % kRing]);
+        __syncwarp();
         if (nt == 0) continue;
         const int kb = ku & 1;
         ok = mbar_sleep(&k_full[kb], (ku >> 1) & 1, abort_flag, p.status);
@@ -527,12 +528,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     while (ok) {
       const int slot = nu % kRing;
-      ok = __all_sync(0xffffffffu, mbar_sleep(&u_full[slot], (nu / kRing) & 1, abort_flag, p.status));
+      ok = mbar_sleep_warp(&u_full[slot], (nu / kRing) & 1, abort_flag, p.status);
       if (!ok) break;
       Unit x;
       read_unit(x, ring + slot * kUnitInts);
+      x.nt = uniform(x.nt);
+      x.key0 = uniform(x.key0);
+      x.len = uniform(x.len);
+      x.r0 = uniform(x.r0);
+      x.r_min = uniform(x.r_min);
+      x.i = uniform(x.i);
       __syncwarp();
       if (lane == 0) mbar_arrive(&u_empty[slot]);
+      __syncwarp();
       ++nu;
       if (x.nt < 0) break;
       const int tile0 = x.key0 + 128 * s, key = tile0 + row;
@@ -552,6 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool lr = mbar_try_wait(&l_full[st], lh), sr = mbar_try_wait(&s_full[2 * s + buf], sh);
         ok = lr || mbar_sleep(&l_full[st], lh, abort_flag, p.status);
         ok &= sr || mbar_sleep(&s_full[2 * s + buf], sh, abort_flag, p.status);
+        __syncwarp();
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
         const float* nl = sLse + 128 * st + 64 * half;
@@ -567,9 +576,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&s_empty[2 * s + buf]);
+          __syncwarp();
           sum32(vb, nl + 32, p.scale_log2, a);
           __syncwarp();
           if (lane == 0) mbar_arrive(&l_empty[st]);
+          __syncwarp();
         } else {
           const int chunks = (min(cols - 64 * half, 64) + 31) >> 5;
 #pragma unroll 1
@@ -594,6 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&s_empty[2 * s + buf]);
             mbar_arrive(&l_empty[st]);
           }
+          __syncwarp();
         }
         // compensated: the tile's sum joins the key's
         const float y = ((a[0] + a[1]) + (a[2] + a[3])) - comp;
@@ -607,6 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the halves join
       float* hs = half_sum + 256 * (nu & 1) + 128 * s;
       if (half) hs[row] = acc;
+      __syncwarp();
       named_barrier_sync(1 + 4 * s + (warp & 3), 64);
       if (!half) acc += hs[row];
       if (!half && key < p.C) {
