@@ -12,6 +12,7 @@ library is missing, :func:`lib` raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -413,30 +414,68 @@ _DTYPES = {torch.bfloat16: PSA_BF16, torch.float16: PSA_FP16}
 
 
 def _dtype16(name, t):
-    if t.dtype not in _DTYPES:
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
         raise ValueError(f"{name} must be bfloat16 or float16, got {t.dtype}")
-    return _DTYPES[t.dtype]
+    return dt
 
 
 def _shape4(name, t):
     if t.dim() != 4:
         raise ValueError(f"{name} must have 4 dimensions, got {tuple(t.shape)}")
-    return tuple(t.shape)
+    return t.shape
 
 
-def _serve_ws(fn, n, device):
+def _arg(name, t, like, shape, dtype):
+    """The address of a tensor argument, checked against the problem (None
+    stays None).  A serving call takes microseconds on the device, so the
+    accepted case is one comparison each."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != like.get_device() or not t.is_contiguous() \
+            or not t.is_cuda:
+        _expect(name, t, like, shape, dtype)
+        _ptr(t)
+    return t.data_ptr()
+
+
+def _serve(fn, like, stream, *args):
+    """Call a serving entry point on the problem's device and stream."""
+    dev = like.get_device()
+    s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+    if dev == torch.cuda.current_device():
+        status = getattr(lib(), fn)(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(lib(), fn)(*args, s)
+    if status != PSA_OK:
+        raise PSAError(fn, status)
+
+
+def _serve_ws(ws, need, like):
+    if ws is None:
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=like.device)
+    elif ws.dtype is not torch.uint8 or ws.numel() < need or ws.get_device() != like.get_device() \
+            or not ws.is_contiguous() or not ws.is_cuda:
+        _expect("ws", ws, like, dtype=torch.uint8, min_numel=need)
+        _ptr(ws)
+    return ws
+
+
+def _new_ws(fn, n, device):
     if n == 0:
         raise PSAError(fn, PSA_ERR_ARG)
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
 
+@functools.lru_cache(maxsize=256)
 def psa_decode_workspace_size(B: int, Hq: int, Hkv: int, T: int, d: int, Bp: int = 1, P: int = 0, C: int = 0) -> int:
     return int(lib().psa_decode_workspace_size(B, Hq, Hkv, T, d, Bp, P, C))
 
 
 def decode_workspace(B, Hq, Hkv, T, d, Bp=1, P=0, C=0, device=None) -> torch.Tensor:
     """A device workspace of psa_decode_workspace_size bytes."""
-    return _serve_ws("psa_decode_workspace_size", psa_decode_workspace_size(B, Hq, Hkv, T, d, Bp, P, C), device)
+    return _new_ws("psa_decode_workspace_size", psa_decode_workspace_size(B, Hq, Hkv, T, d, Bp, P, C), device)
 
 
 def psa_decode(q, k_cache=None, v_cache=None, cache_len=None, k_prefix=None, v_prefix=None, prefix_len=None,
@@ -455,49 +494,40 @@ def psa_decode(q, k_cache=None, v_cache=None, cache_len=None, k_prefix=None, v_p
     Bp, P, C, Hkv = 1, 0, 0, 0
     if k_prefix is not None:
         Bp, Hkv, P, _ = _shape4("k_prefix", k_prefix)
-        _expect("k_prefix", k_prefix, q, (Bp, Hkv, P, d), q.dtype)
         if v_prefix is None:
             raise ValueError("v_prefix is required with k_prefix")
-        _expect("v_prefix", v_prefix, q, (Bp, Hkv, P, d), q.dtype)
-        _expect("prefix_len", prefix_len, q, (Bp,), torch.int32)
     elif v_prefix is not None or prefix_len is not None:
         raise ValueError("v_prefix and prefix_len need k_prefix")
     if k_cache is not None:
         _, Hc, C, _ = _shape4("k_cache", k_cache)
         Hkv = Hkv or Hc
-        _expect("k_cache", k_cache, q, (B, Hkv, C, d), q.dtype)
         if v_cache is None:
             raise ValueError("v_cache is required with k_cache")
-        _expect("v_cache", v_cache, q, (B, Hkv, C, d), q.dtype)
-        _expect("cache_len", cache_len, q, (B,), torch.int32)
     elif v_cache is not None or cache_len is not None:
         raise ValueError("v_cache and cache_len need k_cache")
-    need = psa_decode_workspace_size(B, Hq, Hkv, T, d, Bp, P, C)
-    if ws is None:
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-    _expect("ws", ws, q, dtype=torch.uint8, min_numel=need)
+    pre, own = (Bp, Hkv, P, d), (B, Hkv, C, d)
+    args = (_arg("k_prefix", k_prefix, q, pre, q.dtype), _arg("v_prefix", v_prefix, q, pre, q.dtype),
+            _arg("prefix_len", prefix_len, q, (Bp,), torch.int32), _arg("k_cache", k_cache, q, own, q.dtype),
+            _arg("v_cache", v_cache, q, own, q.dtype), _arg("cache_len", cache_len, q, (B,), torch.int32))
+    ws = _serve_ws(ws, psa_decode_workspace_size(B, Hq, Hkv, T, d, Bp, P, C), q)
     if out is None:
         out = torch.empty_like(q)
-    else:
-        _expect("out", out, q, (B, Hq, T, d), q.dtype)
-    if lse is None:
-        if want_lse:
-            lse = torch.empty(B, Hq, T, dtype=torch.float32, device=q.device)
-    else:
-        _expect("lse", lse, q, (B, Hq, T), torch.float32)
-    _call("psa_decode", q, _ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(prefix_len), _ptr(k_cache), _ptr(v_cache),
-          _ptr(cache_len), B, Hq, Hkv, T, d, Bp, P, C, dt, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
-          _stream(stream, q))
+    if lse is None and want_lse:
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
+    _serve("psa_decode", q, stream, _arg("q", q, q, (B, Hq, T, d), q.dtype), *args, B, Hq, Hkv, T, d, Bp, P, C, dt,
+           _arg("out", out, q, (B, Hq, T, d), q.dtype), _arg("lse", lse, q, (B, Hq, T), torch.float32),
+           ws.data_ptr(), ws.numel())
     return (out, lse) if lse is not None else out
 
 
+@functools.lru_cache(maxsize=256)
 def psa_key_weight_workspace_size(B: int, Hq: int, Hkv: int, T: int, d: int, Bk: int, C: int) -> int:
     return int(lib().psa_key_weight_workspace_size(B, Hq, Hkv, T, d, Bk, C))
 
 
 def key_weight_workspace(B, Hq, Hkv, T, d, Bk, C, device=None) -> torch.Tensor:
     """A device workspace of psa_key_weight_workspace_size bytes."""
-    return _serve_ws("psa_key_weight_workspace_size", psa_key_weight_workspace_size(B, Hq, Hkv, T, d, Bk, C), device)
+    return _new_ws("psa_key_weight_workspace_size", psa_key_weight_workspace_size(B, Hq, Hkv, T, d, Bk, C), device)
 
 
 def psa_key_weight(q, k, lse, key_len=None, causal: bool = False, score=None, ws=None, out=None, stream=None):
@@ -510,32 +540,28 @@ def psa_key_weight(q, k, lse, key_len=None, causal: bool = False, score=None, ws
     B, Hq, T, d = _shape4("q", q)
     dt = _dtype16("q", q)
     Bk, Hkv, C, _ = _shape4("k", k)
-    _expect("k", k, q, (Bk, Hkv, C, d), q.dtype)
     if lse is None:
         raise ValueError("lse (float32 [B, Hq, T]) of the queries is required")
-    _expect("lse", lse, q, (B, Hq, T), torch.float32)
-    _expect("key_len", key_len, q, (Bk,), torch.int32)
-    _expect("score", score, q, (Bk, Hkv, C), torch.float32)
-    need = psa_key_weight_workspace_size(B, Hq, Hkv, T, d, Bk, C)
-    if ws is None:
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-    _expect("ws", ws, q, dtype=torch.uint8, min_numel=need)
+    slots = (Bk, Hkv, C)
+    args = (_arg("q", q, q, (B, Hq, T, d), q.dtype), _arg("k", k, q, (Bk, Hkv, C, d), q.dtype),
+            _arg("lse", lse, q, (B, Hq, T), torch.float32), _arg("key_len", key_len, q, (Bk,), torch.int32),
+            _arg("score", score, q, slots, torch.float32))
+    ws = _serve_ws(ws, psa_key_weight_workspace_size(B, Hq, Hkv, T, d, Bk, C), q)
     if out is None:
-        out = torch.empty(Bk, Hkv, C, dtype=torch.float32, device=q.device)
-    else:
-        _expect("out", out, q, (Bk, Hkv, C), torch.float32)
-    _call("psa_key_weight", q, _ptr(q), _ptr(k), _ptr(lse), _ptr(key_len), _ptr(score), B, Hq, Hkv, T, d, Bk, C,
-          int(causal), dt, _ptr(out), _ptr(ws), ws.numel(), _stream(stream, q))
+        out = torch.empty(slots, dtype=torch.float32, device=q.device)
+    _serve("psa_key_weight", q, stream, *args, B, Hq, Hkv, T, d, Bk, C, int(causal), dt,
+           _arg("out", out, q, slots, torch.float32), ws.data_ptr(), ws.numel())
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def psa_cache_evict_workspace_size(B: int, Hkv: int, C: int, budget: int) -> int:
     return int(lib().psa_cache_evict_workspace_size(B, Hkv, C, budget))
 
 
 def cache_evict_workspace(B, Hkv, C, budget, device=None) -> torch.Tensor:
     """A device workspace of psa_cache_evict_workspace_size bytes."""
-    return _serve_ws("psa_cache_evict_workspace_size", psa_cache_evict_workspace_size(B, Hkv, C, budget), device)
+    return _new_ws("psa_cache_evict_workspace_size", psa_cache_evict_workspace_size(B, Hkv, C, budget), device)
 
 
 def psa_cache_evict(k, v, score, budget: int, pos=None, cache_len=None, sink: int = 0, recent: int = 0, ws=None,
@@ -550,32 +576,27 @@ def psa_cache_evict(k, v, score, budget: int, pos=None, cache_len=None, sink: in
     themselves as the first four the eviction is in place."""
     B, Hkv, C, d = _shape4("k", k)
     _dtype16("k", k)
-    _expect("v", v, k, (B, Hkv, C, d), k.dtype)
-    _expect("score", score, k, (B, Hkv, C), torch.float32)
-    _expect("pos", pos, k, (B, Hkv, C), torch.int32)
-    _expect("cache_len", cache_len, k, (B,), torch.int32)
     need = psa_cache_evict_workspace_size(B, Hkv, C, budget)
-    if ws is None:
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=k.device)
-    _expect("ws", ws, k, dtype=torch.uint8, min_numel=need)
+    full = (B, Hkv, C, d)
+    args = (_arg("k", k, k, full, k.dtype), _arg("v", v, k, full, k.dtype),
+            _arg("score", score, k, (B, Hkv, C), torch.float32), _arg("pos", pos, k, (B, Hkv, C), torch.int32),
+            _arg("cache_len", cache_len, k, (B,), torch.int32))
+    ws = _serve_ws(ws, need, k)
     if out is None:
         if need == 0:
             raise PSAError("psa_cache_evict", PSA_ERR_ARG if budget <= 0 else PSA_ERR_SHAPE)
-        new = lambda *s, dtype: torch.empty(*s, dtype=dtype, device=k.device)  # noqa: E731
+        new = lambda *s, dtype: torch.empty(s, dtype=dtype, device=k.device)  # noqa: E731
         out = (new(B, Hkv, budget, d, dtype=k.dtype), new(B, Hkv, budget, d, dtype=k.dtype),
                new(B, Hkv, budget, dtype=torch.float32), new(B, Hkv, budget, dtype=torch.int32),
                new(B, dtype=torch.int32), new(B, Hkv, budget, dtype=torch.int32))
     k_out, v_out, score_out, pos_out, len_out, kept = out
     C_out = _shape4("k_out", k_out)[2]
-    _expect("k_out", k_out, k, (B, Hkv, C_out, d), k.dtype)
-    _expect("v_out", v_out, k, (B, Hkv, C_out, d), k.dtype)
-    _expect("score_out", score_out, k, (B, Hkv, C_out), torch.float32)
-    _expect("pos_out", pos_out, k, (B, Hkv, C_out), torch.int32)
-    _expect("len_out", len_out, k, (B,), torch.int32)
-    _expect("kept", kept, k, (B, Hkv, budget), torch.int32)
-    _call("psa_cache_evict", k, _ptr(k), _ptr(v), _ptr(score), _ptr(pos), _ptr(cache_len), B, Hkv, C, d, budget,
-          sink, recent, C_out, _ptr(k_out), _ptr(v_out), _ptr(score_out), _ptr(pos_out), _ptr(len_out), _ptr(kept),
-          _ptr(ws), ws.numel(), _stream(stream, k))
+    rows, slots = (B, Hkv, C_out, d), (B, Hkv, C_out)
+    _serve("psa_cache_evict", k, stream, *args, B, Hkv, C, d, budget, sink, recent, C_out,
+           _arg("k_out", k_out, k, rows, k.dtype), _arg("v_out", v_out, k, rows, k.dtype),
+           _arg("score_out", score_out, k, slots, torch.float32), _arg("pos_out", pos_out, k, slots, torch.int32),
+           _arg("len_out", len_out, k, (B,), torch.int32), _arg("kept", kept, k, (B, Hkv, budget), torch.int32),
+           ws.data_ptr(), ws.numel())
     return k_out, v_out, score_out, pos_out, len_out, kept
 
 
