@@ -109,14 +109,12 @@ __device__ __forceinline__ bool seg_bad(const Params& p, int s) {
 }
 // Length of a segment on the line: its row tiles times its key tiles (the
 // last unit of a KV head has one row tile when their number is odd).
-__device__ __forceinline__ long long seg_work(const Params& p, int s) {
-  return static_cast<long long>((seg_len(p, s) + 127) / 128) * p.Hkv * (s < p.npre ? p.pre_rt : p.own_rt);
+__device__ __forceinline__ int seg_work(const Params& p, int s, int len) {
+  return (len + 127) / 128 * p.Hkv * (s < p.npre ? p.pre_rt : p.own_rt);
 }
 // Key tiles of a unit (from `o` on the line, w = 1 or 2 per tile) before x:
 // a cut inside a tile leaves it to the run it starts in.
-__device__ __forceinline__ long long tiles_before(long long x, long long o, int w) {
-  return w == 1 ? x - o : (x - o + 1) >> 1;
-}
+__device__ __forceinline__ int tiles_before(int x, int o, int w) { return w == 1 ? x - o : (x - o + 1) >> 1; }
 
 __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
   const long long t0 = clock64();
@@ -176,9 +174,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = bars + 36;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc + 320);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* start_seg = reinterpret_cast<int*>(tmem_slot + 2);                         // [2] where the runs start,
-  long long* start_off = reinterpret_cast<long long*>(smem + C::kOffMisc + 336);  // [2] and its place on the line
-  long long* red = start_off + 2;                                                 // [20]
   volatile int* ring = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 512); // [kRing][kPieceInts]
 
   const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
@@ -224,176 +219,151 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_launch();
   grid_dep_wait();
 
-  // ---- schedule: the lines' lengths, then where this CTA's runs start
-  long long x0[2], x1[2];
-  bool bad = false;
-#pragma unroll
-  for (int line = 0; line < 2; ++line) {
-    const int sa = line ? p.npre : 0, sb = line ? p.nseg : p.npre;
-    long long mine = 0;
-    for (int s = sa + threadIdx.x; s < sb; s += kThreads) {
-      mine += seg_work(p, s);
-      bad |= blockIdx.x == 0 && seg_bad(p, s);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    __syncthreads();
-    if (lane == 0) red[warp] = mine;
-    __syncthreads();
-    long long total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) total += red[w];
-    // no empty runs between others: every CTA between a unit's first and its
-    // last one writes that unit's parts
-    const long long g = min(total, static_cast<long long>(gridDim.x)), c = blockIdx.x;
-    x0[line] = c < g ? total * c / g : 0;
-    x1[line] = c < g ? total * (c + 1) / g : 0;
-    long long run = 0;
-    for (int s0 = sa; s0 < sb && x0[line] < x1[line]; s0 += kThreads) {
-      const int s = s0 + threadIdx.x;
-      const long long t = s < sb ? seg_work(p, s) : 0;
-      long long inc = t;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += u;
-      }
-      __syncthreads();
-      if (lane == 31) red[warp] = inc;
-      __syncthreads();
-      long long base = run;
-      for (int w = 0; w < kThreads / 32; ++w) {
-        base += w < warp ? red[w] : 0;
-        run += red[w];
-      }
-      const long long lo = base + inc - t, hi = base + inc;
-      if (lo <= x0[line] && x0[line] < hi) {
-        start_seg[line] = s;
-        start_off[line] = lo;
-      }
-    }
-  }
-  bad = __syncthreads_or(bad);
-  // the call's first write of the status word
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = bad ? kStatusLength : 0;
-
   if (warp < 4) {
     reg_dealloc<kRegsProducer>();
     if (warp == 0) {
       // ---------------------------------------------------- scheduler, Q and K loads
       int tiles = 0, items = 0, qpos = 0, np = 0, kl = 0, ql = 0;
       bool ok = true;
-      for (int turn = 0; turn < 2; ++turn) {
-      const int line = turn;
-      long long x = line ? x0[1] : x0[0], off = start_off[line];
-      const long long xe = line ? x1[1] : x1[0];
-      int s = start_seg[line];
-      int lens = 0, lens0 = -64;  // lane l holds the length of segment lens0 + l
-      while (ok && x < xe) {
-        if (s - lens0 >= 32) {
-          lens0 = s;
-          lens = s + lane < p.nseg ? seg_len(p, s + lane) : 0;
-        }
-        const int len = __shfl_sync(0xffffffffu, lens, s - lens0);
-        const int nkt = (len + 127) / 128;
-        const bool pre = s < p.npre;
-        const int up = pre ? p.pre_up : p.own_up, rt = pre ? p.pre_rt : p.own_rt;
-        const long long per_head = static_cast<long long>(nkt) * rt, here = per_head * p.Hkv;
-        if (x >= off + here) {
-          off += here;
-          ++s;
-          continue;
-        }
-        Piece c;
-        c.prefix = pre;
-        c.outer = pre ? s : s - p.npre;
-        c.hkv = static_cast<int>((x - off) / per_head);
-        const long long head0 = off + c.hkv * per_head;
-        const int u = static_cast<int>((x - head0) / (2 * nkt));  // every unit before the last is a pair
-        const int lu = c.hkv * up + u;
-        c.tile0 = 2 * u;
-        c.pair = c.tile0 + 1 < rt;
-        const long long o0 = head0 + 2LL * u * nkt, o1 = o0 + static_cast<long long>(nkt) * (1 + c.pair);
-        c.j0 = static_cast<int>(tiles_before(x, o0, 1 + c.pair));
-        c.nt = static_cast<int>(tiles_before(min(o1, xe), o0, 1 + c.pair)) - c.j0;
-        x = min(o1, xe);
-        c.len = len;
-        const int unit = c.outer * p.Hkv * up + lu;
-        c.slot = unit + static_cast<int>(blockIdx.x);
-        if (c.nt == 0) {
-          // the rest of a tile that the run before took: parts without terms
-          const int rows = 2 * (pre ? p.pre_nb * p.pre_rb : p.own_rb);
-          float2* ml = p.part_ml + (pre ? 0 : p.pre_slots) + static_cast<long long>(c.slot) * rows;
-          for (int i = lane; i < rows; i += 32) ml[i] = make_float2(-INFINITY, 0.f);
-          continue;
-        }
-        if (lane == 0) {
-          int2* uc = p.unit_ctas + (pre ? 0 : p.own_unit0) + unit;
-          if (c.j0 == 0) uc->x = static_cast<int>(blockIdx.x);
-          if (c.j0 + c.nt == nkt) uc->y = static_cast<int>(blockIdx.x);
-        }
-        c.tiles = tiles;
-        c.items = items;
-        c.qpos = qpos;
-        if (lane == 0) {
-          const int slot = np % kRing;
-          if (np >= kRing) ok = mbar_sleep(&pc_empty[slot], ((np / kRing) - 1) & 1, abort_flag, p.status);
-          if (ok) {
-            const int* w = reinterpret_cast<const int*>(&c);
-            for (int i = 0; i < kPieceInts; ++i) ring[slot * kPieceInts + i] = w[i];
-            mbar_arrive(&pc_full[slot]);
-          }
-          // Q
-          const CUtensorMap* mq = c.prefix ? &tmQp : &tmQc;
-          for (int i = 0; i <= c.pair && ok; ++i) {
-            const int qs = (qpos + i) & 1, n = (qpos + i) >> 1;
-            ok = mbar_sleep(&q_empty[qs], (n & 1) ^ 1, abort_flag, p.status);
-            if (!ok) break;
-            const int tile = c.tile0 + i;
-            int r = 0, b;
-            uint32_t rows;
-            if (c.prefix) {
-              if (p.GT >= 128) {
-                const int per = (p.GT + 127) / 128;
-                b = c.outer * p.n + tile / per;
-                r = tile % per * 128;
-              } else {
-                b = c.outer * p.n + tile * p.pre_nb;
-              }
-              rows = static_cast<uint32_t>(p.pre_nb * p.pre_rb);
-            } else {
-              b = c.outer;
-              r = tile * 128;
-              rows = static_cast<uint32_t>(p.own_rb);
-            }
-            mbar_arrive_expect_tx(&q_full[qs], rows * 128 * C::kChunks);
+      for (int line = 0; line < 2; ++line) {
+        const int sa = line ? p.npre : 0, sb = line ? p.nseg : p.npre;
+        // the line's length, and this CTA's run of it: no empty runs between
+        // others, since every CTA between a unit's first and its last one
+        // writes that unit's parts
+        int mine = 0;
+        for (int s = sa + lane; s < sb; s += 32) mine += seg_work(p, s, seg_len(p, s));
+        const int total = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(mine)));
+        const int g = min(total, static_cast<int>(gridDim.x)), cta = static_cast<int>(blockIdx.x);
+        if (cta >= g) continue;
+        const int q = total / g, more = total - q * g;
+        int x = cta * q + min(cta, more);
+        const int xe = x + q + (cta < more ? 1 : 0);
+        // the segment in which it starts, and that segment's place
+        int lens0 = sa, lens = 0, off = 0, s = sa;  // lane l holds the length of segment lens0 + l
+        for (;; lens0 += 32) {
+          lens = lens0 + lane < sb ? seg_len(p, lens0 + lane) : 0;
+          const int w = lens0 + lane < sb ? seg_work(p, lens0 + lane, lens) : 0;
+          int inc = w;
 #pragma unroll
-            for (int ch = 0; ch < C::kChunks; ++ch)
-              tma_load_4d(mq, sQ + qs * C::kTile + ch * 16384, &q_full[qs], 64 * ch, r, c.hkv, b);
-            ql = qpos + i + 1;
+          for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += u;
           }
-          // K
-          const CUtensorMap* mk = c.prefix ? &tmKp : &tmKc;
-          for (int j = 0; j < c.nt && ok; ++j) {
-            const int st = (tiles + j) % kSt, n = (tiles + j) / kSt;
-            ok = mbar_sleep(&k_empty[st], (n & 1) ^ 1, abort_flag, p.status);
-            if (!ok) break;
-            const int y = 128 * (c.j0 + j);
-            const int halves = c.len - y > 64 ? 2 : 1;
-            mbar_arrive_expect_tx(&k_full[st], halves * 64 * 128 * C::kChunks);
-            for (int h = 0; h < halves; ++h)
+          const uint32_t past = __ballot_sync(0xffffffffu, off + inc > x);
+          if (past) {
+            const int owner = __ffs(past) - 1;
+            s = lens0 + owner;
+            off += __shfl_sync(0xffffffffu, inc - w, owner);
+            break;
+          }
+          off += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        while (ok && x < xe) {
+          if (s - lens0 >= 32) {
+            lens0 = s;
+            lens = s + lane < sb ? seg_len(p, s + lane) : 0;
+          }
+          const int len = __shfl_sync(0xffffffffu, lens, s - lens0);
+          const int nkt = (len + 127) / 128;
+          const bool pre = s < p.npre;
+          const int up = pre ? p.pre_up : p.own_up, rt = pre ? p.pre_rt : p.own_rt;
+          const int per_head = nkt * rt, here = per_head * p.Hkv;
+          if (x >= off + here) {
+            off += here;
+            ++s;
+            continue;
+          }
+          Piece c;
+          c.prefix = pre;
+          c.outer = pre ? s : s - p.npre;
+          c.hkv = (x - off) / per_head;
+          const int head0 = off + c.hkv * per_head;
+          const int u = (x - head0) / (2 * nkt);  // every unit before the last is a pair
+          const int lu = c.hkv * up + u;
+          c.tile0 = 2 * u;
+          c.pair = c.tile0 + 1 < rt;
+          const int o0 = head0 + 2 * u * nkt, o1 = o0 + nkt * (1 + c.pair);
+          c.j0 = tiles_before(x, o0, 1 + c.pair);
+          c.nt = tiles_before(min(o1, xe), o0, 1 + c.pair) - c.j0;
+          x = min(o1, xe);
+          c.len = len;
+          const int unit = c.outer * p.Hkv * up + lu;
+          c.slot = unit + static_cast<int>(blockIdx.x);
+          if (c.nt == 0) {
+            // the rest of a tile that the run before took: parts without terms
+            const int rows = 2 * (pre ? p.pre_nb * p.pre_rb : p.own_rb);
+            float2* ml = p.part_ml + (pre ? 0 : p.pre_slots) + static_cast<long long>(c.slot) * rows;
+            for (int i = lane; i < rows; i += 32) ml[i] = make_float2(-INFINITY, 0.f);
+            continue;
+          }
+          if (lane == 0) {
+            int2* uc = p.unit_ctas + (pre ? 0 : p.own_unit0) + unit;
+            if (c.j0 == 0) uc->x = static_cast<int>(blockIdx.x);
+            if (c.j0 + c.nt == nkt) uc->y = static_cast<int>(blockIdx.x);
+          }
+          c.tiles = tiles;
+          c.items = items;
+          c.qpos = qpos;
+          if (lane == 0) {
+            const int slot = np % kRing;
+            if (np >= kRing) ok = mbar_sleep(&pc_empty[slot], ((np / kRing) - 1) & 1, abort_flag, p.status);
+            if (ok) {
+              const int* w = reinterpret_cast<const int*>(&c);
+              for (int i = 0; i < kPieceInts; ++i) ring[slot * kPieceInts + i] = w[i];
+              mbar_arrive(&pc_full[slot]);
+            }
+            // Q
+            const CUtensorMap* mq = c.prefix ? &tmQp : &tmQc;
+            for (int i = 0; i <= c.pair && ok; ++i) {
+              const int qs = (qpos + i) & 1, n = (qpos + i) >> 1;
+              ok = mbar_sleep(&q_empty[qs], (n & 1) ^ 1, abort_flag, p.status);
+              if (!ok) break;
+              const int tile = c.tile0 + i;
+              int r = 0, b;
+              uint32_t rows;
+              if (c.prefix) {
+                if (p.GT >= 128) {
+                  const int per = (p.GT + 127) / 128;
+                  b = c.outer * p.n + tile / per;
+                  r = tile % per * 128;
+                } else {
+                  b = c.outer * p.n + tile * p.pre_nb;
+                }
+                rows = static_cast<uint32_t>(p.pre_nb * p.pre_rb);
+              } else {
+                b = c.outer;
+                r = tile * 128;
+                rows = static_cast<uint32_t>(p.own_rb);
+              }
+              mbar_arrive_expect_tx(&q_full[qs], rows * 128 * C::kChunks);
 #pragma unroll
               for (int ch = 0; ch < C::kChunks; ++ch)
-                tma_load_3d(mk, sK + st * C::kTile + ch * 16384 + h * 8192, &k_full[st], 64 * ch, y + 64 * h,
-                            c.outer * p.Hkv + c.hkv);
-            kl = tiles + j + 1;
+                tma_load_4d(mq, sQ + qs * C::kTile + ch * 16384, &q_full[qs], 64 * ch, r, c.hkv, b);
+              ql = qpos + i + 1;
+            }
+            // K
+            const CUtensorMap* mk = c.prefix ? &tmKp : &tmKc;
+            for (int j = 0; j < c.nt && ok; ++j) {
+              const int st = (tiles + j) % kSt, n = (tiles + j) / kSt;
+              ok = mbar_sleep(&k_empty[st], (n & 1) ^ 1, abort_flag, p.status);
+              if (!ok) break;
+              const int y = 128 * (c.j0 + j);
+              const int halves = c.len - y > 64 ? 2 : 1;
+              mbar_arrive_expect_tx(&k_full[st], halves * 64 * 128 * C::kChunks);
+              for (int h = 0; h < halves; ++h)
+#pragma unroll
+                for (int ch = 0; ch < C::kChunks; ++ch)
+                  tma_load_3d(mk, sK + st * C::kTile + ch * 16384 + h * 8192, &k_full[st], 64 * ch, y + 64 * h,
+                              c.outer * p.Hkv + c.hkv);
+              kl = tiles + j + 1;
+            }
           }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          tiles += c.nt;
+          items += c.pair ? 2 * c.nt : c.nt;
+          qpos += 1 + c.pair;
+          ++np;
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        tiles += c.nt;
-        items += c.pair ? 2 * c.nt : c.nt;
-        qpos += 1 + c.pair;
-        ++np;
-      }
       }
       if (lane == 0) {
         // the end mark: a piece without tiles
@@ -408,6 +378,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = max(0, ql - 2); t < ql; ++t) mbar_drain(&q_full[t & 1], (t >> 1) & 1);
       }
       __syncwarp();
+    } else if (warp == 3) {
+      if (blockIdx.x == 0) {
+        // one writer of the status word at the start: the lengths
+        bool bad = false;
+        for (int s = lane; s < p.nseg; s += 32) bad |= seg_bad(p, s);
+        bad = __any_sync(0xffffffffu, bad);
+        if (lane == 0) *p.status = bad ? kStatusLength : 0;
+      }
     } else if (warp == 2 && lane == 0) {
       // ---------------------------------------------------- V loads
       int np = 0, vl = 0;
@@ -746,7 +724,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p, ui
     // half 0: the prefix, 1: the cache
     if (half == 0 ? p.npre == 0 : p.nseg == p.npre) continue;
     const int outer = half == 0 ? b / p.n : b;
-    if (seg_len(p, half == 0 ? outer : p.npre + b) == 0) continue;
+    const int len = seg_len(p, half == 0 ? outer : p.npre + b);
     const int up = half == 0 ? p.pre_up : p.own_up, rt = half == 0 ? p.pre_rt : p.own_rt;
     const int stride = half == 0 ? p.pre_nb * p.pre_rb : p.own_rb;
     int tile, x;
@@ -761,6 +739,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p, ui
     const bool pair = (tile | 1) < rt;
     const int unit = (outer * p.Hkv + hkv) * up + (tile >> 1);
     const int2 c = p.unit_ctas[(half == 0 ? 0 : p.own_unit0) + unit];
+    if (len == 0) continue;  // no pieces, and `c` is not this call's
     // a pair's row has one part per CTA (stream tile & 1), another's two
     cnt[half] = (c.y - c.x + 1) * (pair ? 1 : 2);
     step[half] = pair ? 2 * stride : stride;
@@ -861,8 +840,9 @@ bool make_plan(Plan& w, int B, int G, int Hkv, int T, int d, int Bp, int P, int 
   p.own_up = (p.own_rt + 1) / 2;
   w.pre_units = P > 0 ? static_cast<long long>(Bp) * Hkv * p.pre_up : 0;
   w.own_units = C > 0 ? static_cast<long long>(B) * Hkv * p.own_up : 0;
-  const long long tiles = w.pre_units * ((P + 127LL) / 128) + w.own_units * ((C + 127LL) / 128);
-  if (w.pre_units + w.own_units > (1LL << 30) || tiles > (1LL << 50)) return false;
+  const long long work = static_cast<long long>(p.npre) * Hkv * p.pre_rt * ((P + 127LL) / 128) +
+                         (C > 0 ? static_cast<long long>(B) * Hkv * p.own_rt * ((C + 127LL) / 128) : 0);
+  if (w.pre_units + w.own_units > (1LL << 30) || work > (1LL << 30)) return false;
   p.own_unit0 = w.pre_units;
   p.pre_slots = P > 0 ? (w.pre_units + kMaxCtas) * 2 * p.pre_nb * p.pre_rb : 0;
   w.part_rows = p.pre_slots + (C > 0 ? (w.own_units + kMaxCtas) * 2 * p.own_rb : 0);
