@@ -701,16 +701,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 //   out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p.
 // All references are read at once, then the rows of O with their weights
 // known, several in flight per warp; the order of the sums is fixed.
-constexpr int kMergeThreads = 128;
+// W warps per row: 4, or 8 when a row has more than 16 parts or so (a long prefix cut
+// over the whole machine: a warp's reads of O are a chain of round trips).
 constexpr int kMaxParts = 4 * kMaxCtas;  // two per CTA from the prefix, two from the cache
 
-template <int D, bool FP16>
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p, uint16_t* out, float* lse) {
+template <int D, bool FP16, int W>
+__global__ void __launch_bounds__(32 * W) merge_kernel(const Params p, uint16_t* out, float* lse) {
   constexpr int kV = D / 32;  // values per lane
   __shared__ float w[kMaxParts];
   __shared__ int at[kMaxParts];
-  __shared__ float so[4][D];
-  __shared__ float red[4];
+  __shared__ float so[W][D];
+  __shared__ float red[W];
   grid_dep_launch();
   grid_dep_wait();
   const int row = blockIdx.x;  // (b, hkv, r)
@@ -748,7 +749,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p, ui
   }
   const int n = cnt[0] + cnt[1];
   float M = -INFINITY;
-  for (int q = threadIdx.x; q < n; q += kMergeThreads) {
+  for (int q = threadIdx.x; q < n; q += 32 * W) {
     const int a = q < cnt[0] ? first[0] + q * step[0] : first[1] + (q - cnt[0]) * step[1];
     at[q] = a;
     M = fmaxf(M, p.part_ml[a].x);
@@ -757,9 +758,11 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p, ui
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   if (lane == 0) red[warp] = M;
   __syncthreads();
-  M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  M = red[0];
+#pragma unroll
+  for (int i = 1; i < W; ++i) M = fmaxf(M, red[i]);
   float L = 0.f;
-  for (int q = threadIdx.x; q < n; q += kMergeThreads) {
+  for (int q = threadIdx.x; q < n; q += 32 * W) {
     const float2 ml = p.part_ml[at[q]];
     // nothing visible in this part: weight 0, and its O is not read
     const float f = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2_approx(ml.x - M);
@@ -771,12 +774,14 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p, ui
   __syncthreads();
   if (lane == 0) red[warp] = L;
   __syncthreads();
-  L = (red[0] + red[1]) + (red[2] + red[3]);
+  L = 0.f;
+#pragma unroll
+  for (int i = 0; i < W; ++i) L += red[i];
   float acc[kV];
 #pragma unroll
   for (int i = 0; i < kV; ++i) acc[i] = 0.f;
 #pragma unroll 4
-  for (int q = warp; q < n; q += 4) {
+  for (int q = warp; q < n; q += W) {
     const float f = w[q];
     if (f != 0.f) {
       const float* src = p.part_o + static_cast<long long>(at[q]) * D + lane * kV;
@@ -795,8 +800,12 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p, ui
   const bool empty = M == -INFINITY && L == 0.f;
   const int i = 2 * threadIdx.x;
   if (i < D) {
-    const float a0 = (so[0][i] + so[1][i]) + (so[2][i] + so[3][i]);
-    const float a1 = (so[0][i + 1] + so[1][i + 1]) + (so[2][i + 1] + so[3][i + 1]);
+    float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      a0 += so[k][i];
+      a1 += so[k][i + 1];
+    }
     const uint32_t u = empty ? 0u : pack_16x2<FP16>(a0 / L, a1 / L);
     *reinterpret_cast<uint32_t*>(out + static_cast<long long>(row) * D + i) = u;
   }
@@ -866,8 +875,13 @@ cudaError_t run(const DecodeLaunch& a, const Plan& w, const CUtensorMap (&m)[6],
   const cudaError_t e2 = launch_chained(decode_kernel<D, FP16>, dim3(grid), dim3(kThreads), Cfg<D>::kSmem, st, m[0],
                                         m[1], m[2], m[3], m[4], m[5], w.p);
   if (e2 != cudaSuccess) return e2;
-  return launch_chained(merge_kernel<D, FP16>, dim3(static_cast<unsigned>(a.B) * a.Hkv * w.p.GT), dim3(kMergeThreads),
-                        0, st, w.p, static_cast<uint16_t*>(a.out), a.lse);
+  const unsigned rows = static_cast<unsigned>(a.B) * a.Hkv * w.p.GT;
+  // CTAs that share one unit's keys, two parts each
+  const long long units = w.pre_units > 0 ? w.pre_units : w.own_units;
+  uint16_t* out = static_cast<uint16_t*>(a.out);
+  if (2 * grid > 16 * units)
+    return launch_chained(merge_kernel<D, FP16, 8>, dim3(rows), dim3(256), 0, st, w.p, out, a.lse);
+  return launch_chained(merge_kernel<D, FP16, 4>, dim3(rows), dim3(128), 0, st, w.p, out, a.lse);
 }
 
 }  // namespace
