@@ -432,16 +432,17 @@ def _arg(name, t, like, shape, dtype):
     accepted case is one comparison each."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != like.get_device() or not t.is_contiguous() \
-            or not t.is_cuda:
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != like.get_device() or not t.is_contiguous():
         _expect(name, t, like, shape, dtype)
-        _ptr(t)
+        raise ValueError("tensor must be contiguous")
     return t.data_ptr()
 
 
 def _serve(fn, like, stream, *args):
     """Call a serving entry point on the problem's device and stream."""
-    dev = like.get_device()
+    dev = like.get_device()   # every other tensor is on it too
+    if dev < 0:
+        raise ValueError("tensor must live on a CUDA device")
     s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
     if dev == torch.cuda.current_device():
         status = getattr(lib(), fn)(*args, s)
@@ -456,9 +457,9 @@ def _serve_ws(ws, need, like):
     if ws is None:
         ws = torch.empty(max(need, 256), dtype=torch.uint8, device=like.device)
     elif ws.dtype is not torch.uint8 or ws.numel() < need or ws.get_device() != like.get_device() \
-            or not ws.is_contiguous() or not ws.is_cuda:
+            or not ws.is_contiguous():
         _expect("ws", ws, like, dtype=torch.uint8, min_numel=need)
-        _ptr(ws)
+        raise ValueError("tensor must be contiguous")
     return ws
 
 
