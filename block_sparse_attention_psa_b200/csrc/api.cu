@@ -591,7 +591,21 @@ int psa_decode(const void* q, const void* k_prefix, const void* v_prefix, const 
       misaligned(v_cache, 16) || misaligned(out, 16) || misaligned(lse, 4) || misaligned(prefix_len, 4) ||
       misaligned(cache_len, 4) || misaligned(workspace, 256))
     return PSA_ERR_ARG;
-  if (workspace_bytes < psa::decode_workspace_bytes(B, Hq / Hkv, Hkv, T, d, Bp, P, C)) return PSA_ERR_CAPACITY;
+  const size_t need = psa::decode_workspace_bytes(B, Hq / Hkv, Hkv, T, d, Bp, P, C);
+  if (workspace_bytes < need) return PSA_ERR_CAPACITY;
+  // outputs over inputs or each other (q itself may become out)
+  const size_t rows = static_cast<size_t>(B) * Hq * T, pre = static_cast<size_t>(Bp) * Hkv * P * d * 2,
+               own = static_cast<size_t>(B) * Hkv * C * d * 2;
+  const Range ins[] = {{k_prefix, pre}, {v_prefix, pre}, {prefix_len, static_cast<size_t>(Bp) * 4},
+                       {k_cache, own},  {v_cache, own},  {cache_len, static_cast<size_t>(B) * 4}};
+  const Range outs[] = {{out, rows * d * 2}, {lse, rows * 4}, {workspace, need}};
+  for (int i = 0; i < 3; ++i) {
+    for (const Range& r : ins)
+      if (overlap(outs[i], r)) return PSA_ERR_ARG;
+    if (!(i == 0 && out == q) && overlap(outs[i], {q, rows * d * 2})) return PSA_ERR_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], outs[j])) return PSA_ERR_ARG;
+  }
   if ((s = check_device({q, k_prefix, k_cache, out, workspace})) !=
       PSA_OK)
     return s;

@@ -526,7 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int step = p.nb * p.rb;
     int nu = 0, qt = 0;
     bool ok = true;
-    while (ok) {
+    const int pair_bar = 1 + 4 * s + (warp & 3);  // named barrier of the two warps of a row
+    for (;;) {
       const int slot = nu % kRing;
       ok = mbar_sleep_warp(&u_full[slot], (nu / kRing) & 1, abort_flag, p.status);
       if (!ok) break;
@@ -620,7 +621,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* hs = half_sum + 256 * (nu & 1) + 128 * s;
       if (half) hs[row] = acc;
       __syncwarp();
-      named_barrier_sync(1 + 4 * s + (warp & 3), 64);
+      named_barrier_sync(pair_bar, 64);
+      if (*abort_flag) {
+        ok = true;  // the barrier was this warp's last
+        break;
+      }
       if (!half) acc += hs[row];
       if (!half && key < p.C) {
         if (p.Z > 1) {
@@ -630,6 +635,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    // After a timeout the two warps of a row meet once more: one that gave up
+    // here, or at the barrier of its unit, where it then sees the flag.
+    if (!ok) named_barrier_sync(pair_bar, 64);
     // units of a line end at the keys: the slots of the pairs behind them
     if (!p.by_head && p.Z == 1) {
       const int tid = threadIdx.x - 128;

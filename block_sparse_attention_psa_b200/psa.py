@@ -438,12 +438,13 @@ def _arg(name, t, like, shape, dtype):
     return t.data_ptr()
 
 
-def _serve(fn, like, stream, *args):
-    """Call a serving entry point on the problem's device and stream."""
+def _serve(fn, like, *args):
+    """Call a serving entry point on the problem's device and its current
+    stream."""
     dev = like.get_device()   # every other tensor is on it too
     if dev < 0:
         raise ValueError("tensor must live on a CUDA device")
-    s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+    s = torch._C._cuda_getCurrentRawStream(dev)
     if dev == torch.cuda.current_device():
         status = getattr(lib(), fn)(*args, s)
     else:
@@ -488,6 +489,9 @@ def psa_decode(q, k_cache=None, v_cache=None, cache_len=None, k_prefix=None, v_p
     last T valid cache entries are the new tokens (query t sees slots below
     cache_len - (T - 1 - t)).  Returns out and, if requested, lse (float32
     [B, Hq, T])."""
+    if stream is not None:   # what is allocated here then belongs to that stream
+        with torch.cuda.stream(stream):
+            return psa_decode(q, k_cache, v_cache, cache_len, k_prefix, v_prefix, prefix_len, ws, out, lse, want_lse)
     B, Hq, T, d = _shape4("q", q)
     dt = _dtype16("q", q)
     if k_cache is None and k_prefix is None:
@@ -515,7 +519,7 @@ def psa_decode(q, k_cache=None, v_cache=None, cache_len=None, k_prefix=None, v_p
         out = torch.empty_like(q)
     if lse is None and want_lse:
         lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
-    _serve("psa_decode", q, stream, _arg("q", q, q, (B, Hq, T, d), q.dtype), *args, B, Hq, Hkv, T, d, Bp, P, C, dt,
+    _serve("psa_decode", q, _arg("q", q, q, (B, Hq, T, d), q.dtype), *args, B, Hq, Hkv, T, d, Bp, P, C, dt,
            _arg("out", out, q, (B, Hq, T, d), q.dtype), _arg("lse", lse, q, (B, Hq, T), torch.float32),
            ws.data_ptr(), ws.numel())
     return (out, lse) if lse is not None else out
@@ -538,6 +542,9 @@ def psa_key_weight(q, k, lse, key_len=None, causal: bool = False, score=None, ws
     (groups of B / Bk sequences read one key set; causal: token t sees slots
     below key_len - (T - 1 - t)).  Slots past ``key_len`` get 0.  ``out`` may
     be ``score`` itself."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return psa_key_weight(q, k, lse, key_len, causal, score, ws, out)
     B, Hq, T, d = _shape4("q", q)
     dt = _dtype16("q", q)
     Bk, Hkv, C, _ = _shape4("k", k)
@@ -550,7 +557,7 @@ def psa_key_weight(q, k, lse, key_len=None, causal: bool = False, score=None, ws
     ws = _serve_ws(ws, psa_key_weight_workspace_size(B, Hq, Hkv, T, d, Bk, C), q)
     if out is None:
         out = torch.empty(slots, dtype=torch.float32, device=q.device)
-    _serve("psa_key_weight", q, stream, *args, B, Hq, Hkv, T, d, Bk, C, int(causal), dt,
+    _serve("psa_key_weight", q, *args, B, Hq, Hkv, T, d, Bk, C, int(causal), dt,
            _arg("out", out, q, slots, torch.float32), ws.data_ptr(), ws.numel())
     return out
 
@@ -575,6 +582,9 @@ def psa_cache_evict(k, v, score, budget: int, pos=None, cache_len=None, sink: in
     [B] and kept [B, Hkv, budget], the slot each entry came from (-1 past the
     length).  ``out`` gives these six buffers instead; with the inputs
     themselves as the first four the eviction is in place."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return psa_cache_evict(k, v, score, budget, pos, cache_len, sink, recent, ws, out)
     B, Hkv, C, d = _shape4("k", k)
     _dtype16("k", k)
     need = psa_cache_evict_workspace_size(B, Hkv, C, budget)
@@ -593,7 +603,7 @@ def psa_cache_evict(k, v, score, budget: int, pos=None, cache_len=None, sink: in
     k_out, v_out, score_out, pos_out, len_out, kept = out
     C_out = _shape4("k_out", k_out)[2]
     rows, slots = (B, Hkv, C_out, d), (B, Hkv, C_out)
-    _serve("psa_cache_evict", k, stream, *args, B, Hkv, C, d, budget, sink, recent, C_out,
+    _serve("psa_cache_evict", k, *args, B, Hkv, C, d, budget, sink, recent, C_out,
            _arg("k_out", k_out, k, rows, k.dtype), _arg("v_out", v_out, k, rows, k.dtype),
            _arg("score_out", score_out, k, slots, torch.float32), _arg("pos_out", pos_out, k, slots, torch.int32),
            _arg("len_out", len_out, k, (B,), torch.int32), _arg("kept", kept, k, (B, Hkv, budget), torch.int32),

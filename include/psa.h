@@ -338,7 +338,8 @@ PSA_API int psa_attn_noalloc(const psa_bf16_t* q, const psa_bf16_t* k, const psa
  * A row that sees no key gives out = 0, lse = -inf.  Rows of K and V past a
  * length may hold anything, NaN included; the new tokens' values must be
  * finite (a masked one is multiplied by zero).  P = 0 (no prefix: its
- * pointers NULL) or C = 0 (no caches), not both; T <= 256.
+ * pointers NULL) or C = 0 (no caches), not both; T <= 256.  out may be q;
+ * any other overlap of an output is refused.
  * Softmax terms are rounded to `dtype` for the tensor cores; sums and the
  * combination of parts are float32.
  * Errors: PSA_ERR_ARG, PSA_ERR_SHAPE (Hq % Hkv, B % Bp, sizes too big),

@@ -9,14 +9,14 @@ import torch
 
 from block_sparse_attention_psa_b200 import psa
 
-FAKE = 1 << 20      # aligned to everything, never dereferenced
-FAR = 1 << 40
+FAR = 1 << 40       # aligned to everything, never dereferenced
+FAKE = FAR // 2
 BIG = 1 << 62
 
 
 def decode(L, **kw):
-    a = dict(q=FAKE, kp=None, vp=None, pl=None, kc=FAKE, vc=FAKE, cl=None, B=2, Hq=4, Hkv=2, T=1, d=64, Bp=1, P=0,
-             C=100, dtype=0, out=FAKE, lse=None, ws=FAKE, n=BIG, st=None)
+    a = dict(q=FAKE, kp=None, vp=None, pl=None, kc=2 * FAR, vc=3 * FAR, cl=None, B=2, Hq=4, Hkv=2, T=1, d=64, Bp=1, P=0,
+             C=100, dtype=0, out=4 * FAR, lse=None, ws=5 * FAR, n=BIG, st=None)
     a.update(kw)
     return L.psa_decode(*a.values())
 
@@ -44,8 +44,11 @@ def evict(L, **kw):
     (dict(C=-1), psa.PSA_ERR_ARG), (dict(dtype=2), psa.PSA_ERR_ARG), (dict(d=96), psa.PSA_ERR_UNSUPPORTED),
     (dict(T=257), psa.PSA_ERR_UNSUPPORTED), (dict(C=(1 << 20) + 1), psa.PSA_ERR_UNSUPPORTED),
     (dict(Hq=5), psa.PSA_ERR_SHAPE), (dict(Bp=2, B=3), psa.PSA_ERR_SHAPE), (dict(B=1 << 24, Hq=4), psa.PSA_ERR_SHAPE),
-    (dict(q=FAKE + 2), psa.PSA_ERR_ARG), (dict(kc=FAKE + 8), psa.PSA_ERR_ARG), (dict(lse=FAKE + 2), psa.PSA_ERR_ARG),
+    (dict(q=FAKE + 2), psa.PSA_ERR_ARG), (dict(kc=2 * FAR + 8), psa.PSA_ERR_ARG), (dict(lse=FAKE + 2), psa.PSA_ERR_ARG),
     (dict(cl=FAKE + 1), psa.PSA_ERR_ARG), (dict(ws=FAKE + 16), psa.PSA_ERR_ARG), (dict(n=1000), psa.PSA_ERR_CAPACITY),
+    # outputs over inputs or each other
+    (dict(out=FAKE + 64), psa.PSA_ERR_ARG), (dict(out=2 * FAR), psa.PSA_ERR_ARG), (dict(lse=3 * FAR), psa.PSA_ERR_ARG),
+    (dict(lse=4 * FAR + 8), psa.PSA_ERR_ARG), (dict(cl=4 * FAR), psa.PSA_ERR_ARG), (dict(ws=2 * FAR), psa.PSA_ERR_ARG),
 ])
 def test_decode_refuses(kw, status):
     assert decode(psa.lib(), **kw) == status
