@@ -80,7 +80,7 @@ struct Params {
   float scale_log2;
   long long pre_slots; // slots of the prefix region: the caches' parts start behind it
   long long own_unit0; // place of the caches' units in unit_ctas
-  int2* unit_ctas;     // per unit: the CTAs that have its first and its last key tile
+  int2* unit_ctas;     // per unit: the runs that have its first and its last key tile
   float* part_o;       // parts: rows x d
   float2* part_ml;     // reference (log2 units), sum
   int* status;
@@ -94,7 +94,7 @@ struct Piece {
   int pair;       // 1: both streams read every key tile, for two row tiles
   int j0, nt;     // key tiles
   int len;        // valid keys of the segment
-  int slot;       // unit + CTA within the region: the place of its parts
+  int slot;       // unit + run within the region: the place of its parts
   int tiles, items, qpos;  // running counts of this CTA at the piece's start
 };
 constexpr int kPieceInts = sizeof(Piece) / 4;
@@ -108,13 +108,17 @@ __device__ __forceinline__ bool seg_bad(const Params& p, int s) {
   return p.cache_len && (p.cache_len[s - p.npre] < 0 || p.cache_len[s - p.npre] > p.C);
 }
 // Length of a segment on the line: its row tiles times its key tiles (the
-// last unit of a KV head has one row tile when their number is odd).
-__device__ __forceinline__ int seg_work(const Params& p, int s, int len) {
-  return (len + 127) / 128 * p.Hkv * (s < p.npre ? p.pre_rt : p.own_rt);
+// last unit of a KV head has one row tile when their number is odd), and
+// `pad` for each unit.
+__device__ __forceinline__ int seg_work(const Params& p, int s, int len, int pad) {
+  const bool pre = s < p.npre;
+  return len == 0 ? 0 : p.Hkv * ((len + 127) / 128 * (pre ? p.pre_rt : p.own_rt) + pad * (pre ? p.pre_up : p.own_up));
 }
-// Key tiles of a unit (from `o` on the line, w = 1 or 2 per tile) before x:
-// a cut inside a tile leaves it to the run it starts in.
-__device__ __forceinline__ int tiles_before(int x, int o, int w) { return w == 1 ? x - o : (x - o + 1) >> 1; }
+// Key tiles of a unit (whose tiles start at `o` on the line, w = 1 or 2 per
+// tile) before x: a cut inside a tile leaves it to the run it starts in.
+__device__ __forceinline__ int tiles_before(int x, int o, int w) {
+  return x <= o ? 0 : (w == 1 ? x - o : (x - o + 1) >> 1);
+}
 
 __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
   const long long t0 = clock64();
@@ -230,10 +234,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the line's length, and this CTA's run of it: no empty runs between
         // others, since every CTA between a unit's first and its last one
         // writes that unit's parts
-        int mine = 0;
-        for (int s = sa + lane; s < sb; s += 32) mine += seg_work(p, s, seg_len(p, s));
-        const int total = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(mine)));
-        const int g = min(total, static_cast<int>(gridDim.x)), cta = static_cast<int>(blockIdx.x);
+        int tile_sum = 0, unit_sum = 0;
+        for (int s = sa + lane; s < sb; s += 32) {
+          const int len = seg_len(p, s);
+          tile_sum += seg_work(p, s, len, 0);
+          unit_sum += len > 0 ? p.Hkv * (line ? p.own_up : p.pre_up) : 0;
+        }
+        tile_sum = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(tile_sum)));
+        unit_sum = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(unit_sum)));
+        // A unit's start and end cost about as much as a tile, and count as one
+        // on the line (a batch of ragged caches without it: the CTAs with two
+        // units were done after 93 us, those with eleven after 103); not where
+        // a run is only a few tiles, which the pads would make uneven.
+        const int pad = tile_sum >= 4 * static_cast<int>(gridDim.x) ? 1 : 0;
+        const int total = tile_sum + pad * unit_sum;
+        // the second line is dealt from the last CTA backwards, so that not
+        // the same ones get the longer runs of both
+        const int g = min(total, static_cast<int>(gridDim.x));
+        const int cta = line ? static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x);
         if (cta >= g) continue;
         const int q = total / g, more = total - q * g;
         int x = cta * q + min(cta, more);
@@ -242,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int lens0 = sa, lens = 0, off = 0, s = sa;  // lane l holds the length of segment lens0 + l
         for (;; lens0 += 32) {
           lens = lens0 + lane < sb ? seg_len(p, lens0 + lane) : 0;
-          const int w = lens0 + lane < sb ? seg_work(p, lens0 + lane, lens) : 0;
+          const int w = lens0 + lane < sb ? seg_work(p, lens0 + lane, lens, pad) : 0;
           int inc = w;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -267,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int nkt = (len + 127) / 128;
           const bool pre = s < p.npre;
           const int up = pre ? p.pre_up : p.own_up, rt = pre ? p.pre_rt : p.own_rt;
-          const int per_head = nkt * rt, here = per_head * p.Hkv;
+          const int per_head = nkt > 0 ? nkt * rt + pad * up : 0, here = per_head * p.Hkv;
           if (x >= off + here) {
             off += here;
             ++s;
@@ -278,19 +296,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           c.outer = pre ? s : s - p.npre;
           c.hkv = (x - off) / per_head;
           const int head0 = off + c.hkv * per_head;
-          const int u = (x - head0) / (2 * nkt);  // every unit before the last is a pair
+          const int u = (x - head0) / (pad + 2 * nkt);  // every unit before the last is a pair
           const int lu = c.hkv * up + u;
           c.tile0 = 2 * u;
           c.pair = c.tile0 + 1 < rt;
-          const int o0 = head0 + 2 * u * nkt, o1 = o0 + nkt * (1 + c.pair);
+          const int o0 = head0 + u * (pad + 2 * nkt) + pad, o1 = o0 + nkt * (1 + c.pair);
           c.j0 = tiles_before(x, o0, 1 + c.pair);
           c.nt = tiles_before(min(o1, xe), o0, 1 + c.pair) - c.j0;
           x = min(o1, xe);
           c.len = len;
           const int unit = c.outer * p.Hkv * up + lu;
-          c.slot = unit + static_cast<int>(blockIdx.x);
+          c.slot = unit + cta;
           if (c.nt == 0) {
-            // the rest of a tile that the run before took: parts without terms
+            // the rest of a tile that the run before took, or a unit's start
+            // alone: parts without terms
             const int rows = 2 * (pre ? p.pre_nb * p.pre_rb : p.own_rb);
             float2* ml = p.part_ml + (pre ? 0 : p.pre_slots) + static_cast<long long>(c.slot) * rows;
             for (int i = lane; i < rows; i += 32) ml[i] = make_float2(-INFINITY, 0.f);
@@ -298,8 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (lane == 0) {
             int2* uc = p.unit_ctas + (pre ? 0 : p.own_unit0) + unit;
-            if (c.j0 == 0) uc->x = static_cast<int>(blockIdx.x);
-            if (c.j0 + c.nt == nkt) uc->y = static_cast<int>(blockIdx.x);
+            if (c.j0 == 0) uc->x = cta;
+            if (c.j0 + c.nt == nkt) uc->y = cta;
           }
           c.tiles = tiles;
           c.items = items;
