@@ -39,6 +39,18 @@
 //  * V rows past a sequence's length are cleared in shared memory before the
 //    product (0 x NaN would reach the sum); K rows past it only touch columns
 //    that are masked.
+// Measured on one B200 (device time, a call in a stream of calls; floors from
+// 6.54 TB/s and 1658 TFLOP/s): 64 ragged caches of up to 4096, 8 KV heads of 4
+// query heads, d = 128: 95 us, 5.8 TB/s (floor 85). 16 samples of a 32K prompt:
+// 43 us (23): 22 us of streaming at the DRAM's rate, the rest is the schedule
+// (1.7), the first load (3), the last tile's chain (5), the imbalance of the
+// SMs (4) and the join (7). 64 sequences of 64 heads over a 128K prefix: 282 to
+// 300 us, 920 to 980 TFLOP/s (166): a pair of items takes ~3280 cycles, set by
+// one stream's chain S -> softmax (2030: 128 exponentials of a thread alone are
+// 1024) -> PV -> S, the tensor core working 2048 of them, under the power cap
+// (1.4 GHz). Tried and slower there: the softmax of a row over two
+// warpgroups, a share of the exponentials on the FMA pipe, terms formed before
+// the new maximum is known.
 // Every wait is bounded.
 #include "internal.h"
 #include "sm100.cuh"
@@ -716,32 +728,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ merge
-// One output row per block: with M the largest reference of its parts,
+// With M the largest reference of a row's parts,
 //   out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p.
-// All references are read at once, then the rows of O with their weights
-// known, several in flight per warp; the order of the sums is fixed.
-// W warps per row: 4, or 8 when a row has more than 16 parts or so (a long prefix cut
-// over the whole machine: a warp's reads of O are a chain of round trips).
-constexpr int kMaxParts = 4 * kMaxCtas;  // two per CTA from the prefix, two from the cache
+// A row's parts are its prefix unit's and its cache unit's, one (pair) or two
+// per run that has tiles of the unit; the order of the sums is fixed.
 
-template <int D, bool FP16, int W>
-__global__ void __launch_bounds__(32 * W) merge_kernel(const Params p, uint16_t* out, float* lse) {
-  constexpr int kV = D / 32;  // values per lane
-  __shared__ float w[kMaxParts];
-  __shared__ int at[kMaxParts];
-  __shared__ float so[W][D];
-  __shared__ float red[W];
-  grid_dep_launch();
-  grid_dep_wait();
-  const int row = blockIdx.x;  // (b, hkv, r)
-  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+// Where the parts of output row `row` = (b, hkv, r) are: part q of segment
+// kind h (0: prefix, 1: cache) at place first[h] + q * step[h].
+struct RowParts {
+  int cnt[2], first[2], step[2];
+};
+__device__ __forceinline__ RowParts row_parts(const Params& p, int row) {
+  RowParts k = {{0, 0}, {0, 0}, {0, 0}};
   const int bh = row / p.GT, r = row - bh * p.GT;
   const int b = bh / p.Hkv, hkv = bh - b * p.Hkv;
-  // where the row's parts are: first CTA, count and place of the first
-  int cnt[2] = {0, 0}, first[2] = {0, 0}, step[2] = {0, 0};
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    // half 0: the prefix, 1: the cache
     if (half == 0 ? p.npre == 0 : p.nseg == p.npre) continue;
     const int outer = half == 0 ? b / p.n : b;
     const int len = seg_len(p, half == 0 ? outer : p.npre + b);
@@ -760,19 +762,109 @@ __global__ void __launch_bounds__(32 * W) merge_kernel(const Params p, uint16_t*
     const int unit = (outer * p.Hkv + hkv) * up + (tile >> 1);
     const int2 c = p.unit_ctas[(half == 0 ? 0 : p.own_unit0) + unit];
     if (len == 0) continue;  // no pieces, and `c` is not this call's
-    // a pair's row has one part per CTA (stream tile & 1), another's two
-    cnt[half] = (c.y - c.x + 1) * (pair ? 1 : 2);
-    step[half] = pair ? 2 * stride : stride;
-    first[half] = static_cast<int>((half == 0 ? 0 : p.pre_slots) + 2LL * (unit + c.x) * stride +
-                                   (pair ? (tile & 1) * stride : 0)) + x;
+    // a pair's row has one part per run (stream tile & 1), another's two
+    k.cnt[half] = (c.y - c.x + 1) * (pair ? 1 : 2);
+    k.step[half] = pair ? 2 * stride : stride;
+    k.first[half] = static_cast<int>((half == 0 ? 0 : p.pre_slots) + 2LL * (unit + c.x) * stride +
+                                     (pair ? (tile & 1) * stride : 0)) + x;
   }
-  const int n = cnt[0] + cnt[1];
+  return k;
+}
+__device__ __forceinline__ int part_at(const RowParts& k, int q) {
+  return q < k.cnt[0] ? k.first[0] + q * k.step[0] : k.first[1] + (q - k.cnt[0]) * k.step[1];
+}
+
+template <int kV>
+__device__ __forceinline__ void add_part(float (&acc)[kV], float f, const float* src) {
+  if constexpr (kV == 4) {
+    const float4 v = *reinterpret_cast<const float4*>(src);
+    acc[0] += f * v.x, acc[1] += f * v.y, acc[2] += f * v.z, acc[3] += f * v.w;
+  } else {
+    const float2 v = *reinterpret_cast<const float2*>(src);
+    acc[0] += f * v.x, acc[1] += f * v.y;
+  }
+}
+
+// Few parts per row: a warp per row, 32 parts at a time.  (4096 rows of 14
+// parts: 22 us with a block of eight warps per row, whose barriers and waves
+// cost more than the parts.)
+template <int D, bool FP16>
+__global__ void __launch_bounds__(128) merge_kernel(const Params p, int rows, uint16_t* out, float* lse) {
+  constexpr int kV = D / 32;  // values per lane
+  grid_dep_launch();
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31;
+  const int row = static_cast<int>(blockIdx.x) * 4 + uniform(threadIdx.x >> 5);
+  if (row >= rows) return;
+  const RowParts k = row_parts(p, row);
+  const int n = uniform(k.cnt[0] + k.cnt[1]);
+  float acc[kV];
+#pragma unroll
+  for (int i = 0; i < kV; ++i) acc[i] = 0.f;
+  float M = -INFINITY, L = 0.f;
+  for (int q0 = 0; q0 < n; q0 += 32) {
+    const int at = q0 + lane < n ? part_at(k, q0 + lane) : 0;
+    const float2 ml = q0 + lane < n ? p.part_ml[at] : make_float2(-INFINITY, 0.f);
+    float top = ml.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    top = fmaxf(top, M);
+    const float old = M == -INFINITY ? (L == 0.f ? 0.f : 1.f) : ex2_approx(M - top);
+    // nothing visible in this part: weight 0, and its O is not read
+    const float f = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2_approx(ml.x - top);
+    float l = f == 0.f ? 0.f : f * ml.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    M = top;
+    L = L * old + l;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) acc[i] *= old;
+    const int m = min(32, n - q0);
+#pragma unroll 8
+    for (int j = 0; j < m; ++j) {
+      const float fj = __shfl_sync(0xffffffffu, f, j);
+      const int aj = __shfl_sync(0xffffffffu, at, j);
+      if (fj != 0.f) add_part<kV>(acc, fj, p.part_o + static_cast<long long>(aj) * D + lane * kV);
+    }
+  }
+  const bool empty = M == -INFINITY && L == 0.f;
+  const float inv = 1.f / L;
+  uint16_t* dst = out + static_cast<long long>(row) * D + lane * kV;
+  if constexpr (kV == 4) {
+    const uint2 u = empty ? make_uint2(0, 0) : make_uint2(pack_16x2<FP16>(acc[0] * inv, acc[1] * inv),
+                                                          pack_16x2<FP16>(acc[2] * inv, acc[3] * inv));
+    *reinterpret_cast<uint2*>(dst) = u;
+  } else {
+    *reinterpret_cast<uint32_t*>(dst) = empty ? 0u : pack_16x2<FP16>(acc[0] * inv, acc[1] * inv);
+  }
+  if (lse && lane == 0) lse[row] = empty ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+// A prefix cut over the whole machine: eight warps per row, whose reads of O
+// would be one warp's chain of round trips (shared 32K prefix, 40 parts: 8 us
+// with four warps, 5 with eight).
+constexpr int kMaxParts = 4 * kMaxCtas;  // two per run of the prefixes, two of the caches
+
+template <int D, bool FP16>
+__global__ void __launch_bounds__(256) merge_wide_kernel(const Params p, uint16_t* out, float* lse) {
+  constexpr int kV = D / 32, W = 8;
+  __shared__ float w[kMaxParts];
+  __shared__ int at[kMaxParts];
+  __shared__ float so[W][D];
+  __shared__ float red[W];
+  grid_dep_launch();
+  grid_dep_wait();
+  const int row = blockIdx.x;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const RowParts k = row_parts(p, row);
+  const int n = uniform(k.cnt[0] + k.cnt[1]);
   float M = -INFINITY;
   for (int q = threadIdx.x; q < n; q += 32 * W) {
-    const int a = q < cnt[0] ? first[0] + q * step[0] : first[1] + (q - cnt[0]) * step[1];
+    const int a = part_at(k, q);
     at[q] = a;
     M = fmaxf(M, p.part_ml[a].x);
   }
+  __syncwarp();
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   if (lane == 0) red[warp] = M;
@@ -783,11 +875,11 @@ __global__ void __launch_bounds__(32 * W) merge_kernel(const Params p, uint16_t*
   float L = 0.f;
   for (int q = threadIdx.x; q < n; q += 32 * W) {
     const float2 ml = p.part_ml[at[q]];
-    // nothing visible in this part: weight 0, and its O is not read
     const float f = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2_approx(ml.x - M);
     w[q] = f;
     if (f != 0.f) L += f * ml.y;
   }
+  __syncwarp();
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
   __syncthreads();
@@ -802,16 +894,7 @@ __global__ void __launch_bounds__(32 * W) merge_kernel(const Params p, uint16_t*
 #pragma unroll 4
   for (int q = warp; q < n; q += W) {
     const float f = w[q];
-    if (f != 0.f) {
-      const float* src = p.part_o + static_cast<long long>(at[q]) * D + lane * kV;
-      if constexpr (kV == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        acc[0] += f * v.x, acc[1] += f * v.y, acc[2] += f * v.z, acc[3] += f * v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        acc[0] += f * v.x, acc[1] += f * v.y;
-      }
-    }
+    if (f != 0.f) add_part<kV>(acc, f, p.part_o + static_cast<long long>(at[q]) * D + lane * kV);
   }
 #pragma unroll
   for (int i = 0; i < kV; ++i) so[warp][lane * kV + i] = acc[i];
@@ -821,9 +904,9 @@ __global__ void __launch_bounds__(32 * W) merge_kernel(const Params p, uint16_t*
   if (i < D) {
     float a0 = 0.f, a1 = 0.f;
 #pragma unroll
-    for (int k = 0; k < W; ++k) {
-      a0 += so[k][i];
-      a1 += so[k][i + 1];
+    for (int j = 0; j < W; ++j) {
+      a0 += so[j][i];
+      a1 += so[j][i + 1];
     }
     const uint32_t u = empty ? 0u : pack_16x2<FP16>(a0 / L, a1 / L);
     *reinterpret_cast<uint32_t*>(out + static_cast<long long>(row) * D + i) = u;
@@ -894,13 +977,20 @@ cudaError_t run(const DecodeLaunch& a, const Plan& w, const CUtensorMap (&m)[6],
   const cudaError_t e2 = launch_chained(decode_kernel<D, FP16>, dim3(grid), dim3(kThreads), Cfg<D>::kSmem, st, m[0],
                                         m[1], m[2], m[3], m[4], m[5], w.p);
   if (e2 != cudaSuccess) return e2;
-  const unsigned rows = static_cast<unsigned>(a.B) * a.Hkv * w.p.GT;
-  // CTAs that share one unit's keys, two parts each
-  const long long units = w.pre_units > 0 ? w.pre_units : w.own_units;
+  const int rows = a.B * a.Hkv * w.p.GT;
+  // parts per row: the runs that share one unit's keys, two of each where a
+  // unit is a single row tile
+  const bool pre = w.pre_units > 0;
+  const long long units = pre ? w.pre_units : w.own_units;
+  const long long parts = (pre ? w.p.pre_rt : w.p.own_rt) > 1 ? grid / units : 2 * grid / units;
   uint16_t* out = static_cast<uint16_t*>(a.out);
-  if (2 * grid > 16 * units)
-    return launch_chained(merge_kernel<D, FP16, 8>, dim3(rows), dim3(256), 0, st, w.p, out, a.lse);
-  return launch_chained(merge_kernel<D, FP16, 4>, dim3(rows), dim3(128), 0, st, w.p, out, a.lse);
+  // few rows leave the machine idle: a block each (two rows of 16 parts 9.0 us a
+  // call against 11.2); many rows of few parts want a warp each
+  if (parts > 16 || (parts > 2 && rows <= 4 * device_sm_count()))
+    return launch_chained(merge_wide_kernel<D, FP16>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, st, w.p, out,
+                          a.lse);
+  return launch_chained(merge_kernel<D, FP16>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, st, w.p,
+                        rows, out, a.lse);
 }
 
 }  // namespace
