@@ -302,7 +302,7 @@ int check_weight_shape(int B, int Hq, int Hkv, int T, int d, int Bk, int C) {
   if (T <= 0 || Bk <= 0 || C <= 0) return PSA_ERR_ARG;
   if (T > kMaxCache || C > kMaxCache) return PSA_ERR_UNSUPPORTED;
   if (B % Bk || static_cast<long long>(Hq / Hkv) * T >= (1LL << 31)) return PSA_ERR_SHAPE;
-  return psa::weight_workspace_bytes(B, Hq / Hkv, Hkv, T, Bk, C) ? PSA_OK : PSA_ERR_SHAPE;
+  return psa::weight_workspace_bytes(B, Hq / Hkv, Hkv, T, d, Bk, C) ? PSA_OK : PSA_ERR_SHAPE;
 }
 
 int check_evict_shape(int B, int Hkv, int C, int budget) {
@@ -634,7 +634,7 @@ int psa_decode(const void* q, const void* k_prefix, const void* v_prefix, const 
 
 size_t psa_key_weight_workspace_size(int B, int Hq, int Hkv, int T, int d, int Bk, int C) {
   if (check_weight_shape(B, Hq, Hkv, T, d, Bk, C) != PSA_OK) return 0;
-  return psa::weight_workspace_bytes(B, Hq / Hkv, Hkv, T, Bk, C);
+  return psa::weight_workspace_bytes(B, Hq / Hkv, Hkv, T, d, Bk, C);
 }
 
 int psa_key_weight(const void* q, const void* k, const float* lse, const int* key_len, const float* score_in, int B,
@@ -648,7 +648,7 @@ int psa_key_weight(const void* q, const void* k, const float* lse, const int* ke
   if (misaligned(q, 16) || misaligned(k, 16) || misaligned(lse, 4) || misaligned(key_len, 4) ||
       misaligned(score_in, 4) || misaligned(score_out, 4) || misaligned(workspace, 256))
     return PSA_ERR_ARG;
-  const size_t need = psa::weight_workspace_bytes(B, Hq / Hkv, Hkv, T, Bk, C);
+  const size_t need = psa::weight_workspace_bytes(B, Hq / Hkv, Hkv, T, d, Bk, C);
   if (workspace_bytes < need) return PSA_ERR_CAPACITY;
   const size_t rows = static_cast<size_t>(B) * Hq * T, slots = static_cast<size_t>(Bk) * Hkv * C;
   const Range out = {score_out, slots * 4};

@@ -197,7 +197,7 @@ struct WeightLaunch {
   bool fp16;
   char* ws;
 };
-size_t weight_workspace_bytes(int B, int G, int Hkv, int T, int Bk, int C);  // 0: too large to schedule
+size_t weight_workspace_bytes(int B, int G, int Hkv, int T, int d, int Bk, int C);  // 0: too large to schedule
 cudaError_t launch_weight(const WeightLaunch& a, cudaStream_t st);
 
 // evict.cu: eviction from a cache by accumulated weight

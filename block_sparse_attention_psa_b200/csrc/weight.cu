@@ -17,7 +17,7 @@
 //    operations and one exponential per (query, key) pair: an SM's tensor
 //    core takes 256 cycles for a tile, its 16 exponentials a cycle 1024, so
 //    it is bound by the exponentials.
-//  * Up to 32 queries per key (decode): stream_kernel. 16 keys x 8 queries per
+//  * Up to 32 queries per key (16 at d = 128; decode): stream_kernel. 16 keys x 8 queries per
 //    mma.sync, with K going from DRAM straight to registers: a thread's four
 //    16-byte pieces of two key rows are its A operands, in an order of the d
 //    features that the queries' registers share. No shared memory and no barriers, so nothing
@@ -47,7 +47,8 @@
 //  * Sums: 128 columns in four fp32 accumulators, tile sums added with a
 //    compensation term (a key of a long prefill sums 10^5 terms).
 // Measured on one B200 (device time): one token of 48 caches of up to 4099,
-// 8 KV heads of 3, d = 64: 27 us, 4.6 TB/s (floor 19 us: the reads of K). Last
+// 8 KV heads of 3, d = 64: 24 us, 5.1 TB/s (floor 19 us: the reads of K; of 64
+// caches of 4096 at d = 128 55 us, 5.9 TB/s). Last
 // 64 queries of a 128K prefill, 8 KV heads of 4, d = 128: 110 us (60:
 // exponentials). A whole 8K causal prefill of 32 heads: 345 us, 800 TFLOP/s
 // (floors: 238 exponentials alone, 166 tensor core). A tile of 128 x 128 x 2
@@ -668,7 +669,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ few queries
-constexpr int kStreamRows = 32;     // queries per key set and KV head, at most
+// Queries per key set and KV head, at most.  32 caches of 4096, 8 KV heads, us a call,
+// this kernel against weight_kernel: d = 64: 12 rows 19 / 37, 28 rows 28 / 37;
+// d = 128: 12 rows 32 / 42, 20 rows 50 / 42.
+template <int D>
+constexpr int kStreamRows = D == 64 ? 32 : 16;
 constexpr int kStreamThreads = 256;
 
 template <bool FP16>
@@ -689,7 +694,7 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t
 // pieces t, t + 4, .. (16 bytes each) of keys g and g + 8, and the same
 // pieces of query g of every group.
 template <int D, bool FP16, int NT>
-__global__ void __launch_bounds__(kStreamThreads, NT == 4 ? 1 : 2)
+__global__ void __launch_bounds__(kStreamThreads, NT == 4 ? 1 : (D == 64 ? 3 : 2))
     stream_kernel(const uint4* __restrict__ q, const uint4* __restrict__ k, const Params p, int chunk, int chunks) {
   constexpr int kP = D / 32;  // pieces per lane and row
   constexpr int kWarps = kStreamThreads / 32;
@@ -898,7 +903,9 @@ cudaError_t run(const Params& p, const CUtensorMap& mq, const CUtensorMap& mk, i
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 size_t lse_bytes(const Params& p) { return static_cast<size_t>(p.Bk) * p.Hkv * p.all * 512; }
 
-bool streams(const Params& p) { return static_cast<long long>(p.n) * p.GT <= kStreamRows; }
+bool streams(const Params& p, int d) {
+  return static_cast<long long>(p.n) * p.GT <= (d == 64 ? kStreamRows<64> : kStreamRows<128>);
+}
 
 template <int D, bool FP16>
 cudaError_t run_stream(const WeightLaunch& a, const Params& p, cudaStream_t st) {
@@ -914,15 +921,17 @@ cudaError_t run_stream(const WeightLaunch& a, const Params& p, cudaStream_t st) 
   const int rows = p.n * p.GT;
   if (rows <= 8) return launch_chained(stream_kernel<D, FP16, 1>, grid, dim3(kStreamThreads), 0, st, q, k, p, chunk, chunks);
   if (rows <= 16) return launch_chained(stream_kernel<D, FP16, 2>, grid, dim3(kStreamThreads), 0, st, q, k, p, chunk, chunks);
-  return launch_chained(stream_kernel<D, FP16, 4>, grid, dim3(kStreamThreads), 0, st, q, k, p, chunk, chunks);
+  if constexpr (kStreamRows<D> > 16)
+    return launch_chained(stream_kernel<D, FP16, 4>, grid, dim3(kStreamThreads), 0, st, q, k, p, chunk, chunks);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-size_t weight_workspace_bytes(int B, int G, int Hkv, int T, int Bk, int C) {
+size_t weight_workspace_bytes(int B, int G, int Hkv, int T, int d, int Bk, int C) {
   Params p = {};
   if (!make_plan(p, B, G, Hkv, T, Bk, C)) return 0;
-  if (streams(p)) return 256;
+  if (streams(p, d)) return 256;
   return 256 + align256(lse_bytes(p)) + align256(p.Z > 1 ? static_cast<size_t>(p.Z) * Bk * Hkv * C * 4 : 0);
 }
 
@@ -938,7 +947,7 @@ cudaError_t launch_weight(const WeightLaunch& a, cudaStream_t st) {
   p.status = reinterpret_cast<int*>(a.ws);
   p.nl = reinterpret_cast<float*>(a.ws + 256);
   p.part = reinterpret_cast<float*>(a.ws + 256 + align256(lse_bytes(p)));
-  if (streams(p)) {
+  if (streams(p, a.d)) {
     if (a.d == 128) return a.fp16 ? run_stream<128, true>(a, p, st) : run_stream<128, false>(a, p, st);
     return a.fp16 ? run_stream<64, true>(a, p, st) : run_stream<64, false>(a, p, st);
   }

@@ -71,6 +71,10 @@ CASES = [
     (10, 1, 30, 1, 5, 64, 260, "fp16", [260], False),               # 150 rows per sequence
     (1, 1, 8, 1, 700, 128, 700, "bf16", [700], True),               # few units: query tiles split
     (4, 1, 2, 1, 200, 64, 300, "bf16", [300], True),                # causal and shared
+    (2, 2, 20, 1, 1, 128, 400, "bf16", [400, 131], True),           # rows on both sides of where the kernels change
+    (2, 2, 20, 1, 1, 64, 400, "fp16", [400, 131], True),
+    (2, 2, 16, 1, 1, 128, 400, "fp16", [17, 399], True),
+    (1, 1, 11, 1, 3, 64, 200, "bf16", [150], True),
 ]
 
 
