@@ -35,6 +35,9 @@
 //  * Query tiles: T >= 128 tokens: 128 tokens of one head, so that causal
 //    tiles past the diagonal are skipped; fewer: up to 128 of the G T rows
 //    that share the KV head, over several sequences when they share the keys.
+//    A head's pairs that lie in one CTA's run make one unit, and where all its
+//    query tiles fit the ring (two, at d = 64 four) they stay for all of them
+//    (64-token window 111 -> 107 us).
 //  * Units of equal cost (T < 128) lie on one line that is cut into equal
 //    runs; a prefill's go to the CTAs in turn, forwards and backwards, heaviest
 //    (fewest keys hidden) first.  When there are fewer units than two per SM the
@@ -49,7 +52,7 @@
 // Measured on one B200 (device time): one token of 48 caches of up to 4099,
 // 8 KV heads of 3, d = 64: 24 us, 5.1 TB/s (floor 19 us: the reads of K; of 64
 // caches of 4096 at d = 128 55 us, 5.9 TB/s). Last
-// 64 queries of a 128K prefill, 8 KV heads of 4, d = 128: 110 us (60:
+// 64 queries of a 128K prefill, 8 KV heads of 4, d = 128: 107 us (60:
 // exponentials). A whole 8K causal prefill of 32 heads: 345 us, 800 TFLOP/s
 // (floors: 238 exponentials alone, 166 tensor core). A tile of 128 x 128 x 2
 // takes 2350 cycles, 1800 of them sums (88% of the exponential unit), the rest
@@ -99,6 +102,7 @@ struct Params {
   int all;                // tiles of a KV head: n G heads' (by_head) or `tiles`
   int N;                  // columns of the products: nb * rb rounded up to 16
   int Z, pairs;
+  int resident;           // a unit's query tiles stay on chip for all its pairs
   long long units;
   float scale_log2;
   int* status;
@@ -111,7 +115,8 @@ struct Unit {
   int i, g, r0;    // first tile: sequence of the group, query head of the KV head (by_head), row
   int r_min;       // by_head: first visible row of every head
   int z;
-  int pad[2];      // a multiple of 16 bytes: read as vectors
+  int np;          // pairs of key tiles, one after the other, with the same query tiles
+  int pad;         // a multiple of 16 bytes: read as vectors
 };
 constexpr int kUnitInts = sizeof(Unit) / 4;
 static_assert(kUnitInts == 12, "");
@@ -185,6 +190,7 @@ __device__ __forceinline__ Unit make_unit(const Params& p, int bh, int pair, int
   x.key0 = 256 * pair;
   x.len = len;
   x.z = z;
+  x.np = 1;
   x.r_min = 0;
   int per = p.tiles, total = p.tiles;
   if (p.by_head) {
@@ -404,7 +410,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           rel -= static_cast<long long>(hkv) * pairs * p.Z;
           int pair = static_cast<int>(rel / p.Z), z = static_cast<int>(rel - static_cast<long long>(pair) * p.Z);
           for (long long x = x0; ok && x < x1; ++x) {
-            ok = publish(make_unit(p, bk * p.Hkv + hkv, pair, z, len));
+            Unit u = make_unit(p, bk * p.Hkv + hkv, pair, z, len);
+            if (p.Z == 1) {
+              // the rest of the head's pairs that lie in the run: one unit
+              u.np = static_cast<int>(min(static_cast<long long>(pairs - pair), x1 - x));
+              x += u.np - 1;
+              pair += u.np - 1;
+            }
+            ok = publish(u);
             if (++z < p.Z) continue;
             z = 0;
             if (++pair < pairs) continue;
@@ -431,33 +444,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         next_unit(x, true);
         if (x.nt < 0 || !ok) break;
         if (x.nt == 0) continue;
-        const int kb = ku & 1;
-        if (!(ok = mbar_sleep(&k_empty[kb], ((ku >> 1) & 1) ^ 1, abort_flag, p.status))) break;
-        // 64-key boxes; none that starts past the length
-        const int boxes = min(4, (x.len - x.key0 + 63) / 64);
-        mbar_arrive_expect_tx(&k_full[kb], boxes * 64 * 128 * C::kChunks);
-        for (int i = 0; i < boxes; ++i)
-#pragma unroll
-          for (int ch = 0; ch < C::kChunks; ++ch)
-            tma_load_3d(&tmK, sK + (2 * kb + (i >> 1)) * C::kTile + ch * 16384 + (i & 1) * 8192, &k_full[kb],
-                        64 * ch, x.key0 + 64 * i, x.bk * p.Hkv + x.hkv);
-        ++ku;
-        Tile t = {x.i, x.g, x.r0};
         const uint32_t bytes = static_cast<uint32_t>(p.nb * p.rb) * 128 * C::kChunks;
         const float* nl = p.nl + (static_cast<long long>(x.bk) * p.Hkv + x.hkv) * p.all * 128;
-        for (int f = 0; f < x.nt; ++f, ++qt) {
-          const int st = qt % kQ;
-          const int lt = qt % kLse;
-          if (!(ok = mbar_sleep(&q_empty[st], ((qt / kQ) & 1) ^ 1, abort_flag, p.status))) break;
-          if (!(ok = mbar_sleep(&l_empty[lt], ((qt / kLse) & 1) ^ 1, abort_flag, p.status))) break;
-          mbar_arrive_expect_tx(&l_full[lt], 512);
-          bulk_load(sLse + 128 * lt, nl + static_cast<long long>(t.index(p)) * 128, 512, &l_full[lt]);
-          mbar_arrive_expect_tx(&q_full[st], bytes);
+        for (int pp = 0; ok && pp < x.np; ++pp) {
+          const int kb = ku & 1, key0 = x.key0 + 256 * pp;
+          if (!(ok = mbar_sleep(&k_empty[kb], ((ku >> 1) & 1) ^ 1, abort_flag, p.status))) break;
+          // 64-key boxes; none that starts past the length
+          const int boxes = min(4, (x.len - key0 + 63) / 64);
+          mbar_arrive_expect_tx(&k_full[kb], boxes * 64 * 128 * C::kChunks);
+          for (int i = 0; i < boxes; ++i)
 #pragma unroll
-          for (int ch = 0; ch < C::kChunks; ++ch)
-            tma_load_4d(&tmQ, sQ + st * C::kTile + ch * 16384, &q_full[st], 64 * ch, t.r0,
-                        p.by_head ? x.hkv * p.G + t.g : x.hkv, x.bk * p.n + t.i);
-          t.next(p, x);
+            for (int ch = 0; ch < C::kChunks; ++ch)
+              tma_load_3d(&tmK, sK + (2 * kb + (i >> 1)) * C::kTile + ch * 16384 + (i & 1) * 8192, &k_full[kb],
+                          64 * ch, key0 + 64 * i, x.bk * p.Hkv + x.hkv);
+          ++ku;
+          if (pp > 0 && p.resident) continue;
+          Tile t = {x.i, x.g, x.r0};
+          for (int f = 0; f < x.nt; ++f, ++qt) {
+            const int st = qt % kQ;
+            const int lt = qt % kLse;
+            if (!(ok = mbar_sleep(&q_empty[st], ((qt / kQ) & 1) ^ 1, abort_flag, p.status))) break;
+            if (!(ok = mbar_sleep(&l_empty[lt], ((qt / kLse) & 1) ^ 1, abort_flag, p.status))) break;
+            mbar_arrive_expect_tx(&l_full[lt], 512);
+            bulk_load(sLse + 128 * lt, nl + static_cast<long long>(t.index(p)) * 128, 512, &l_full[lt]);
+            mbar_arrive_expect_tx(&q_full[st], bytes);
+#pragma unroll
+            for (int ch = 0; ch < C::kChunks; ++ch)
+              tma_load_4d(&tmQ, sQ + st * C::kTile + ch * 16384, &q_full[st], 64 * ch, t.r0,
+                          p.by_head ? x.hkv * p.G + t.g : x.hkv, x.bk * p.n + t.i);
+            t.next(p, x);
+          }
         }
       }
       // no bulk copy may still be writing shared memory when the CTA leaves
@@ -467,58 +483,62 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
       // ---------------------------------------------------- MMA issue
       // The whole warp walks the tiles in step; one elected lane issues.  The
-      // lanes wait without a vote and agree on stopping once per unit.
+      // lanes wait without a vote and agree on stopping once per pair.
       const uint64_t dK0 = sdesc_sw128(smem_u32(sK), 16, 1024);
       const uint64_t dQ0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
       constexpr uint64_t kStep = C::kTile >> 4;
       const uint32_t idesc = idesc_f16_f32(FP16, 128, p.N, 0, 0);
-      int ku = 0, qt = 0;
+      int ku = 0, qt = 0, it = 0;  // pairs, query tiles done with, products
       bool ok = true;
       while (ok) {
         Unit x;
         next_unit(x, false);
         __syncwarp();
-        const int nt = __shfl_sync(0xffffffffu, x.nt, 0);
+        const int nt = uniform(x.nt), np = uniform(x.np);
         if (nt < 0) break;
         if (elect_one()) mbar_arrive(&u_empty[(nu - 1) % kRing]);
         __syncwarp();
         if (nt == 0) continue;
-        const int kb = ku & 1;
-        ok = mbar_sleep(&k_full[kb], (ku >> 1) & 1, abort_flag, p.status);
-        for (int f = 0; f < nt; ++f, ++qt) {
-          const int st = qt % kQ, buf = qt & 1;
-          const uint32_t eh = ((qt >> 1) & 1) ^ 1, qh = (qt / kQ) & 1;
-          // one look at all three barriers, whose latencies then overlap
-          const bool rq = mbar_try_wait(&q_full[st], qh), r0 = mbar_try_wait(&s_empty[buf], eh),
-                     r1 = mbar_try_wait(&s_empty[2 + buf], eh);
-          const uint64_t a = dK0 + 2 * kb * kStep, b = dQ0 + st * kStep;
-          if (!rq) ok &= mbar_sleep(&q_full[st], qh, abort_flag, p.status);
-          if (!r0) ok &= mbar_sleep(&s_empty[buf], eh, abort_flag, p.status);
-          __syncwarp();
-          tc_fence_after();
-          if (elect_one()) {
+        for (int pp = 0; ok && pp < np; ++pp) {
+          const bool release = !p.resident || pp == np - 1;  // of the query tiles
+          const int kb = ku & 1;
+          ok = mbar_sleep(&k_full[kb], (ku >> 1) & 1, abort_flag, p.status);
+          for (int f = 0; f < nt; ++f, ++it) {
+            const int st = (qt + f) % kQ, buf = it & 1;
+            const uint32_t eh = ((it >> 1) & 1) ^ 1, qh = ((qt + f) / kQ) & 1;
+            // one look at all three barriers, whose latencies then overlap
+            const bool rq = mbar_try_wait(&q_full[st], qh), r0 = mbar_try_wait(&s_empty[buf], eh),
+                       r1 = mbar_try_wait(&s_empty[2 + buf], eh);
+            const uint64_t a = dK0 + 2 * kb * kStep, b = dQ0 + st * kStep;
+            if (!rq) ok &= mbar_sleep(&q_full[st], qh, abort_flag, p.status);
+            if (!r0) ok &= mbar_sleep(&s_empty[buf], eh, abort_flag, p.status);
+            __syncwarp();
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              tc_mma_bf16(tbase + 128 * buf, a + (kk >> 2) * 1024 + (kk & 3) * 2,
-                          b + (kk >> 2) * 1024 + (kk & 3) * 2, idesc, kk ? 1u : 0u);
-            tc_commit(&s_full[buf]);
-          }
-          if (!r1) ok &= mbar_sleep(&s_empty[2 + buf], eh, abort_flag, p.status);
-          __syncwarp();
-          tc_fence_after();
-          if (elect_one()) {
+              for (int kk = 0; kk < D / 16; ++kk)
+                tc_mma_bf16(tbase + 128 * buf, a + (kk >> 2) * 1024 + (kk & 3) * 2,
+                            b + (kk >> 2) * 1024 + (kk & 3) * 2, idesc, kk ? 1u : 0u);
+              tc_commit(&s_full[buf]);
+            }
+            if (!r1) ok &= mbar_sleep(&s_empty[2 + buf], eh, abort_flag, p.status);
+            __syncwarp();
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              tc_mma_bf16(tbase + 256 + 128 * buf, a + kStep + (kk >> 2) * 1024 + (kk & 3) * 2,
-                          b + (kk >> 2) * 1024 + (kk & 3) * 2, idesc, kk ? 1u : 0u);
-            tc_commit(&s_full[2 + buf]);
-            tc_commit(&q_empty[st]);
-            if (f == nt - 1) tc_commit(&k_empty[kb]);
+              for (int kk = 0; kk < D / 16; ++kk)
+                tc_mma_bf16(tbase + 256 + 128 * buf, a + kStep + (kk >> 2) * 1024 + (kk & 3) * 2,
+                            b + (kk >> 2) * 1024 + (kk & 3) * 2, idesc, kk ? 1u : 0u);
+              tc_commit(&s_full[2 + buf]);
+              if (release) tc_commit(&q_empty[st]);
+              if (f == nt - 1) tc_commit(&k_empty[kb]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          if (release) qt += nt;
+          ok = __all_sync(0xffffffffu, ok);
+          ++ku;
         }
-        ok = __all_sync(0xffffffffu, ok);
-        ++ku;
       }
       if (elect_one()) {
         tc_commit(drain);
@@ -534,8 +554,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_addr = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256 * s + 64 * half;
     const int lim = p.by_head ? p.T : (p.GT >= 128 ? p.GT : p.n * p.GT);
     const int step = p.nb * p.rb;
-    int nu = 0, qt = 0;
-    bool ok = true;
+    int nu = 0, qt = 0, it = 0, joins = 0;
+    bool ok = true, met = false;
     const int pair_bar = 1 + 4 * s + (warp & 3);  // named barrier of the two warps of a row
     for (;;) {
       const int slot = nu % kRing;
@@ -549,105 +569,112 @@ __global__ void __launch_bounds__(kThreads, 1)
       x.r0 = uniform(x.r0);
       x.r_min = uniform(x.r_min);
       x.i = uniform(x.i);
+      x.np = uniform(x.np);
       __syncwarp();
       if (lane == 0) mbar_arrive(&u_empty[slot]);
       __syncwarp();
       ++nu;
       if (x.nt < 0) break;
-      const int tile0 = x.key0 + 128 * s, key = tile0 + row;
-      const long long at = static_cast<long long>(x.bk * p.Hkv + x.hkv) * p.C + key;
-      const float before = p.Z == 1 && !half && p.score_in && key < x.len ? p.score_in[at] : 0.f;
-      float acc = 0.f, comp = 0.f;
-      // rows r, r + step, .. below lim, from r_min again for every head
-      int r = p.by_head || p.GT >= 128 ? x.r0 : x.i * p.GT;
-      // first row whose token sees every key of this tile
-      const int r_open = !p.causal ? INT_MIN : tile0 + 127 - (x.len - p.T);
+      for (int pp = 0; pp < x.np; ++pp) {
+        const bool release = !p.resident || pp == x.np - 1;
+        const int tile0 = x.key0 + 256 * pp + 128 * s, key = tile0 + row;
+        const long long at = static_cast<long long>(x.bk * p.Hkv + x.hkv) * p.C + key;
+        const float before = p.Z == 1 && !half && p.score_in && key < x.len ? p.score_in[at] : 0.f;
+        float acc = 0.f, comp = 0.f;
+        // rows r, r + step, .. below lim, from r_min again for every head
+        int r = p.by_head || p.GT >= 128 ? x.r0 : x.i * p.GT;
+        // first row whose token sees every key of this tile
+        const int r_open = !p.causal ? INT_MIN : tile0 + 127 - (x.len - p.T);
 #pragma unroll 1
-      for (int f = 0; f < x.nt; ++f, ++qt) {
-        const int buf = qt & 1, st = qt % kLse;
-        const int cols = min(step, lim - r);
-        const bool mask = (p.by_head ? r : 0) < r_open;
-        const uint32_t lh = (qt / kLse) & 1, sh = (qt >> 1) & 1;
-        const bool lr = mbar_try_wait(&l_full[st], lh), sr = mbar_try_wait(&s_full[2 * s + buf], sh);
-        ok = lr || mbar_sleep(&l_full[st], lh, abort_flag, p.status);
-        ok &= sr || mbar_sleep(&s_full[2 * s + buf], sh, abort_flag, p.status);
-        __syncwarp();
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        tc_fence_after();
-        const float* nl = sLse + 128 * st + 64 * half;
-        const uint32_t src = s_addr + 128 * buf;
-        float a[4] = {0.f, 0.f, 0.f, 0.f};
-        if (!mask && cols == 128) {
-          float va[32], vb[32];
-          tmem_ld32(src, va);
-          tc_wait_ld();
-          tmem_ld32(src + 32, vb);  // on its way meanwhile
-          sum32(va, nl, p.scale_log2, a);
-          tc_wait_ld();
-          tc_fence_before();
+        for (int f = 0; f < x.nt; ++f, ++it) {
+          const int buf = it & 1, st = (qt + f) % kLse;
+          const int cols = min(step, lim - r);
+          const bool mask = (p.by_head ? r : 0) < r_open;
+          const uint32_t lh = ((qt + f) / kLse) & 1, sh = (it >> 1) & 1;
+          const bool lr = mbar_try_wait(&l_full[st], lh), sr = mbar_try_wait(&s_full[2 * s + buf], sh);
+          ok = lr || mbar_sleep(&l_full[st], lh, abort_flag, p.status);
+          ok &= sr || mbar_sleep(&s_full[2 * s + buf], sh, abort_flag, p.status);
           __syncwarp();
-          if (lane == 0) mbar_arrive(&s_empty[2 * s + buf]);
-          __syncwarp();
-          sum32(vb, nl + 32, p.scale_log2, a);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&l_empty[st]);
-          __syncwarp();
-        } else {
-          const int chunks = (min(cols - 64 * half, 64) + 31) >> 5;
-#pragma unroll 1
-          for (int c = 0; c < chunks; ++c) {
-            // last key that the query of column 64 half + 32 c + lane sees;
-            // none where there is no query (its column holds anything)
-            const int col = 64 * half + 32 * c + lane;
-            int last = -1;
-            if (col < cols) last = !mask ? INT_MAX : x.len - p.T + (p.by_head ? r + col : (r + col) % p.T);
-            float v[32];
-            tmem_ld32(src + 32 * c, v);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          tc_fence_after();
+          const float* nl = sLse + 128 * st + 64 * half;
+          const uint32_t src = s_addr + 128 * buf;
+          float a[4] = {0.f, 0.f, 0.f, 0.f};
+          if (!mask && cols == 128) {
+            float va[32], vb[32];
+            tmem_ld32(src, va);
             tc_wait_ld();
+            tmem_ld32(src + 32, vb);  // on its way meanwhile
+            sum32(va, nl, p.scale_log2, a);
+            tc_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_empty[2 * s + buf]);
+            __syncwarp();
+            sum32(vb, nl + 32, p.scale_log2, a);
+            __syncwarp();
+            if (lane == 0 && release) mbar_arrive(&l_empty[st]);
+            __syncwarp();
+          } else {
+            const int chunks = (min(cols - 64 * half, 64) + 31) >> 5;
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c) {
+              // last key that the query of column 64 half + 32 c + lane sees;
+              // none where there is no query (its column holds anything)
+              const int col = 64 * half + 32 * c + lane;
+              int last = -1;
+              if (col < cols) last = !mask ? INT_MAX : x.len - p.T + (p.by_head ? r + col : (r + col) % p.T);
+              float v[32];
+              tmem_ld32(src + 32 * c, v);
+              tc_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float e = ex2_approx(fmaf(v[i], p.scale_log2, nl[32 * c + i]));
-              if (key <= __shfl_sync(0xffffffffu, last, i)) a[i & 3] += e;
+              for (int i = 0; i < 32; ++i) {
+                const float e = ex2_approx(fmaf(v[i], p.scale_log2, nl[32 * c + i]));
+                if (key <= __shfl_sync(0xffffffffu, last, i)) a[i & 3] += e;
+              }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&s_empty[2 * s + buf]);
+              if (release) mbar_arrive(&l_empty[st]);
+            }
+            __syncwarp();
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&s_empty[2 * s + buf]);
-            mbar_arrive(&l_empty[st]);
+          // compensated: the tile's sum joins the key's
+          const float y = ((a[0] + a[1]) + (a[2] + a[3])) - comp;
+          const float z = acc + y;
+          comp = (z - acc) - y;
+          acc = z;
+          r += step;
+          if (r >= lim) r = x.r_min;
+        }
+        if (!ok) break;
+        if (release) qt += x.nt;
+        // the halves join
+        float* hs = half_sum + 256 * (joins & 1) + 128 * s;
+        ++joins;
+        if (half) hs[row] = acc;
+        __syncwarp();
+        named_barrier_sync(pair_bar, 64);
+        if (*abort_flag) {
+          met = true;  // the barrier was this warp's last
+          break;
+        }
+        if (!half) acc += hs[row];
+        if (!half && key < p.C) {
+          if (p.Z > 1) {
+            p.part[static_cast<long long>(x.z) * p.Bk * p.Hkv * p.C + at] = acc;
+          } else {
+            p.score_out[at] = key < x.len ? before + acc : 0.f;
           }
-          __syncwarp();
-        }
-        // compensated: the tile's sum joins the key's
-        const float y = ((a[0] + a[1]) + (a[2] + a[3])) - comp;
-        const float z = acc + y;
-        comp = (z - acc) - y;
-        acc = z;
-        r += step;
-        if (r >= lim) r = x.r_min;
-      }
-      if (!ok) break;
-      // the halves join
-      float* hs = half_sum + 256 * (nu & 1) + 128 * s;
-      if (half) hs[row] = acc;
-      __syncwarp();
-      named_barrier_sync(pair_bar, 64);
-      if (*abort_flag) {
-        ok = true;  // the barrier was this warp's last
-        break;
-      }
-      if (!half) acc += hs[row];
-      if (!half && key < p.C) {
-        if (p.Z > 1) {
-          p.part[static_cast<long long>(x.z) * p.Bk * p.Hkv * p.C + at] = acc;
-        } else {
-          p.score_out[at] = key < x.len ? before + acc : 0.f;
         }
       }
+      if (!ok || met) break;
     }
     // After a timeout the two warps of a row meet once more: one that gave up
     // here, or at the barrier of its unit, where it then sees the flag.
-    if (!ok) named_barrier_sync(pair_bar, 64);
+    if (!ok && !met) named_barrier_sync(pair_bar, 64);
     // units of a line end at the keys: the slots of the pairs behind them
     if (!p.by_head && p.Z == 1) {
       const int tid = threadIdx.x - 128;
@@ -951,6 +978,7 @@ cudaError_t launch_weight(const WeightLaunch& a, cudaStream_t st) {
     if (a.d == 128) return a.fp16 ? run_stream<128, true>(a, p, st) : run_stream<128, false>(a, p, st);
     return a.fp16 ? run_stream<64, true>(a, p, st) : run_stream<64, false>(a, p, st);
   }
+  p.resident = !p.by_head && p.Z == 1 && p.all <= (a.d == 128 ? Cfg<128>::kQStages : Cfg<64>::kQStages);
   CUtensorMap mq, mk;
   const uint64_t u = 1;
   const uint64_t by_kv[4] = {u * a.d, u * p.GT, u * a.Hkv, u * a.B};
