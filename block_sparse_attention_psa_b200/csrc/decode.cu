@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               } else {
                 b = c.outer;
                 r = tile * 128;
-                rows = static_cast<uint32_t>(p.own_rb);
+                rows = 128;
               }
               mbar_arrive_expect_tx(&q_full[qs], rows * 128 * C::kChunks);
 #pragma unroll
@@ -1016,7 +1016,10 @@ cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t st) {
   const uint64_t u = 1;
   const uint64_t dq[4] = {u * a.d, u * p.GT, u * a.Hkv, u * a.B};
   const uint32_t bp[4] = {64, static_cast<uint32_t>(p.pre_rb), 1, static_cast<uint32_t>(p.pre_nb)};
-  const uint32_t bc[4] = {64, static_cast<uint32_t>(p.own_rb), 1, 1};
+  // A cache's box is a whole tile, whose rows past G T come in as zeros: products
+  // of zeros cost less power than products of whatever was there (64 ragged
+  // caches of 4 rows, after 500 calls: 102 -> 98 us).
+  const uint32_t bc[4] = {64, 128, 1, 1};
   const uint32_t bk[3] = {64, 64, 1};
   const uint64_t dp[3] = {u * a.d, u * a.P, u * a.Bp * a.Hkv}, dc[3] = {u * a.d, u * a.C, u * a.B * a.Hkv};
   CUresult r = encode_tensor_map_16(&m[0], a.q, a.fp16, 4, dq, bp);
