@@ -760,8 +760,11 @@ __device__ __forceinline__ RowParts row_parts(const Params& p, int row) {
     }
     const bool pair = (tile | 1) < rt;
     const int unit = (outer * p.Hkv + hkv) * up + (tile >> 1);
-    const int2 c = p.unit_ctas[(half == 0 ? 0 : p.own_unit0) + unit];
+    int2 c = p.unit_ctas[(half == 0 ? 0 : p.own_unit0) + unit];
     if (len == 0) continue;  // no pieces, and `c` is not this call's
+    // after a wait that ran out it may be unwritten: no place past the parts
+    c.x = min(max(c.x, 0), kMaxCtas - 1);
+    c.y = min(max(c.y, c.x), kMaxCtas - 1);
     // a pair's row has one part per run (stream tile & 1), another's two
     k.cnt[half] = (c.y - c.x + 1) * (pair ? 1 : 2);
     k.step[half] = pair ? 2 * stride : stride;
