@@ -10,7 +10,7 @@
 // the queries runs along the columns and is read from shared memory, four
 // columns per broadcast load; lse_kernel lays it out beforehand as the tiles
 // want it (-lse log2 e, -inf in columns without a query), so that a tile's
-// 512 bytes come with one bulk copy.  (A warp that gathered them itself was what
+// 128 words come with one bulk copy, with a mark for columns of -inf.  (A warp that gathered them itself was what
 // a 64-token window waited for: 7000 cycles a unit.)
 //
 //  * Decode reads K once for few queries: bound by DRAM.  A prefill does 2 d
@@ -70,6 +70,7 @@ constexpr int kThreads = 640;      // WG0: K/Q loads, MMA issue, lse loads, unit
 constexpr int kRegsProducer = 64;  // 128 x 64 + 512 x 104 = 640 x 96
 constexpr int kRegsSum = 104;
 constexpr int kLse = 4;            // query tiles whose lse is in shared memory
+constexpr int kNl = 132;           // words of a tile's lse: 128 columns, then per 32 of them whether one is -inf
 constexpr int kRing = 4;           // units in flight
 constexpr int kPlanSms = 148;      // SMs the split is planned for (fixed: it sizes the workspace)
 constexpr int kPoly = 1;           // of eight pairs of exponentials, those on the FMA pipe
@@ -83,7 +84,7 @@ struct Cfg {
   static constexpr int kOffK = 0;               // two pairs of key tiles
   static constexpr int kOffQ = 4 * kTile;
   static constexpr int kOffLse = kOffQ + kQStages * kTile;
-  static constexpr int kOffMisc = kOffLse + kLse * 512;
+  static constexpr int kOffMisc = kOffLse + kLse * kNl * 4;
   static constexpr int kSmem = kOffMisc + 1024 + 2048 + 1024;  // barriers, half sums, alignment slack
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
@@ -94,7 +95,7 @@ struct Params {
   const float* score_in;  // nullable
   float* score_out;
   float* part;            // [Z][Bk * Hkv][C] when Z > 1
-  float* nl;              // [Bk * Hkv][all tiles][128]: -lse log2(e)
+  float* nl;              // [Bk * Hkv][all tiles][kNl]: -lse log2(e)
   int B, G, Hkv, T, Bk, n, C, causal;
   int GT, by_head;        // by_head: query tiles of one head
   int nb, rb;             // query tile: sequences x rows (box)
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sK = smem + C::kOffK;
   uint8_t* sQ = smem + C::kOffQ;
-  float* sLse = reinterpret_cast<float*>(smem + C::kOffLse);  // [kLse][128] -lse in log2 units
+  float* sLse = reinterpret_cast<float*>(smem + C::kOffLse);  // [kLse][kNl] -lse in log2 units
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffMisc);
   uint64_t* k_full = bars + 0;    // [2] a pair of key tiles landed  (TMA)
   uint64_t* k_empty = bars + 2;   // [2] its last product done       (commit)
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* start_bk = reinterpret_cast<int*>(tmem_slot + 2);
   long long* start_off = reinterpret_cast<long long*>(smem + C::kOffMisc + 336);
-  long long* red = start_off + 1;                                                  // [12]
+  long long* red = start_off + 1;                                                  // [kThreads / 32]
   int* ring = reinterpret_cast<int*>(smem + C::kOffMisc + 768);  // [kRing][kUnitInts]
   float* half_sum = reinterpret_cast<float*>(smem + C::kOffMisc + 1024);           // [parity][key tile][128]
 
@@ -445,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (x.nt < 0 || !ok) break;
         if (x.nt == 0) continue;
         const uint32_t bytes = static_cast<uint32_t>(p.nb * p.rb) * 128 * C::kChunks;
-        const float* nl = p.nl + (static_cast<long long>(x.bk) * p.Hkv + x.hkv) * p.all * 128;
+        const float* nl = p.nl + (static_cast<long long>(x.bk) * p.Hkv + x.hkv) * p.all * kNl;
         for (int pp = 0; ok && pp < x.np; ++pp) {
           const int kb = ku & 1, key0 = x.key0 + 256 * pp;
           if (!(ok = mbar_sleep(&k_empty[kb], ((ku >> 1) & 1) ^ 1, abort_flag, p.status))) break;
@@ -465,8 +466,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int lt = qt % kLse;
             if (!(ok = mbar_sleep(&q_empty[st], ((qt / kQ) & 1) ^ 1, abort_flag, p.status))) break;
             if (!(ok = mbar_sleep(&l_empty[lt], ((qt / kLse) & 1) ^ 1, abort_flag, p.status))) break;
-            mbar_arrive_expect_tx(&l_full[lt], 512);
-            bulk_load(sLse + 128 * lt, nl + static_cast<long long>(t.index(p)) * 128, 512, &l_full[lt]);
+            mbar_arrive_expect_tx(&l_full[lt], kNl * 4);
+            bulk_load(sLse + kNl * lt, nl + static_cast<long long>(t.index(p)) * kNl, kNl * 4, &l_full[lt]);
             mbar_arrive_expect_tx(&q_full[st], bytes);
 #pragma unroll
             for (int ch = 0; ch < C::kChunks; ++ch)
@@ -593,17 +594,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t lh = ((qt + f) / kLse) & 1, sh = (it >> 1) & 1;
           const bool lr = mbar_try_wait(&l_full[st], lh), sr = mbar_try_wait(&s_full[2 * s + buf], sh);
           ok = lr || mbar_sleep(&l_full[st], lh, abort_flag, p.status);
+          const float* nl = sLse + kNl * st + 64 * half;
+          // a query without lse adds nothing, whatever its logits (NaN too)
+          const int2 gone = *reinterpret_cast<const int2*>(sLse + kNl * st + 128 + 2 * half);
           ok &= sr || mbar_sleep(&s_full[2 * s + buf], sh, abort_flag, p.status);
           __syncwarp();
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           tc_fence_after();
-          const float* nl = sLse + 128 * st + 64 * half;
           const uint32_t src = s_addr + 128 * buf;
           float a[4] = {0.f, 0.f, 0.f, 0.f};
-          if (!mask && cols == 128) {
-            float va[32], vb[32];
-            tmem_ld32(src, va);
-            tc_wait_ld();
+          // (the first columns are on their way while the marks are read)
+          float va[32];
+          tmem_ld32(src, va);
+          const bool whole = __all_sync(0xffffffffu, !mask && cols == 128 && (gone.x | gone.y) == 0);
+          tc_wait_ld();
+          if (whole) {
+            float vb[32];
             tmem_ld32(src + 32, vb);  // on its way meanwhile
             sum32(va, nl, p.scale_log2, a);
             tc_wait_ld();
@@ -620,10 +626,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
               // last key that the query of column 64 half + 32 c + lane sees;
-              // none where there is no query (its column holds anything)
+              // none where there is no query, or none that counts (its column
+              // holds anything)
               const int col = 64 * half + 32 * c + lane;
               int last = -1;
-              if (col < cols) last = !mask ? INT_MAX : x.len - p.T + (p.by_head ? r + col : (r + col) % p.T);
+              if (col < cols && nl[32 * c + lane] != -INFINITY) last = !mask ? INT_MAX : x.len - p.T + (p.by_head ? r + col : (r + col) % p.T);
               float v[32];
               tmem_ld32(src + 32 * c, v);
               tc_wait_ld();
@@ -772,6 +779,10 @@ __global__ void __launch_bounds__(kStreamThreads, NT == 4 ? 1 : (D == 64 ? 3 : 2
     const uint4* src = q + ((static_cast<long long>(bk * p.n + i) * p.Hkv + hkv) * p.GT + rr) * (D / 8);
 #pragma unroll
     for (int m = 0; m < kP; ++m) qf[j][m] = r < rows ? __ldg(src + t + 4 * m) : make_uint4(0, 0, 0, 0);
+    // a query without lse adds nothing, whatever it holds (NaN too)
+    if (r < rows && __ldg(p.lse + (static_cast<long long>(bk * p.n + i) * p.Hkv + hkv) * p.GT + rr) == -INFINITY)
+#pragma unroll
+      for (int m = 0; m < kP; ++m) qf[j][m] = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r2 = 8 * j + 2 * t + e;
@@ -853,7 +864,10 @@ __global__ void __launch_bounds__(256) lse_kernel(const Params p) {
     if (in) l = __ldg(p.lse + (static_cast<long long>(bk * p.n + i) * p.Hkv + hkv) * p.GT + r);
   }
   // a query that saw nothing (lse -inf) adds nothing
-  p.nl[tile * 128 + c] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+  const bool none = l == -INFINITY;
+  p.nl[tile * kNl + c] = none ? -INFINITY : -l * kLog2e;
+  const bool any = __any_sync(0xffffffffu, none);  // (a warp is 32 columns of one tile)
+  if ((c & 31) == 0) p.nl[tile * kNl + 128 + (c >> 5)] = __int_as_float(any);
 }
 
 // score_out = score_in + the parts of a split unit, in order.
@@ -928,7 +942,7 @@ cudaError_t run(const Params& p, const CUtensorMap& mq, const CUtensorMap& mk, i
 }
 
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
-size_t lse_bytes(const Params& p) { return static_cast<size_t>(p.Bk) * p.Hkv * p.all * 512; }
+size_t lse_bytes(const Params& p) { return static_cast<size_t>(p.Bk) * p.Hkv * p.all * kNl * 4; }
 
 bool streams(const Params& p, int d) {
   return static_cast<long long>(p.n) * p.GT <= (d == 64 ? kStreamRows<64> : kStreamRows<128>);

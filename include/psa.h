@@ -360,8 +360,8 @@ PSA_API int psa_decode(const void* q, const void* k_prefix, const void* v_prefix
  *     of e^{q.k_j / sqrt(d) - lse[b,hq,t]}             (j < key_len)
  *   score_out[bk,h,j] = 0                              (j >= key_len)
  *   q [B,Hq,T,d]; k [Bk,Hkv,C,d]; lse float32 [B,Hq,T] as psa_decode,
- *   psa_dense or psa_attn give it (-inf: the query adds nothing); key_len
- *   [Bk]; B = Bk * n, sequence b reads key set b / n.  Token t sees slot j
+ *   psa_dense or psa_attn give it (-inf: the query adds nothing, whatever it
+ *   holds); key_len [Bk]; B = Bk * n, sequence b reads key set b / n.  Token t sees slot j
  *   iff causal = 0, or j < key_len - (T - 1 - t) (the last T entries are the
  *   tokens themselves: T = key_len is a causal prefill, a small T an
  *   observation window or a decode step).

@@ -94,6 +94,30 @@ def test_without_a_score_and_in_place():
     check(x, [650], True, in_place=True)
 
 
+@pytest.mark.parametrize("case", [
+    (3, 3, 4, 2, 1, 64, 300, "fp16", [300, 100, 257], True),      # few queries
+    (6, 2, 16, 1, 1, 128, 700, "bf16", [700, 300], False),        # 48 rows of a tile
+    (1, 1, 4, 2, 64, 128, 600, "bf16", [600], True),              # a window, whole tiles
+    (2, 2, 4, 2, 256, 64, 500, "bf16", [500, 256], True),         # a prefill
+    (1, 1, 8, 1, 640, 128, 640, "fp16", [640], False),            # split query tiles
+], ids=str)
+@pytest.mark.parametrize("junk", [float("nan"), float("inf"), -float("inf")], ids=str)
+def test_queries_without_lse_add_nothing_whatever_they_hold(case, junk):
+    """Padded queries: lse = -inf, and the row's memory as it was."""
+    B, Bk, Hq, Hkv, T, d, C, dt, lens, causal = case
+    q, k, lse, score = make(B, Bk, Hq, Hkv, T, d, C, {"bf16": torch.bfloat16, "fp16": torch.float16}[dt], lens, causal)
+    gone = torch.rand(lse.shape, generator=torch.Generator().manual_seed(5)) < 0.3
+    gone[0, 0, 0], gone[-1, -1, -1] = True, False
+    lse[gone] = -float("inf")
+    zeros = torch.where(gone[..., None], 0, q)
+    ref = torch.nan_to_num(k.double()), lse.double().numpy()
+    ref, mass = O.key_weight(zeros.double().numpy(), ref[0].numpy(), ref[1], lens, causal, score.double().numpy())
+    q = torch.where(gone[..., None], torch.full_like(q, junk), q)
+    got = psa.psa_key_weight(q.cuda(), k.cuda(), lse.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                             causal=causal, score=score.cuda()).double().cpu().numpy()
+    assert (np.abs(got - ref) <= 3e-4 * mass + 2.0 ** -23 * np.abs(ref)).all()
+
+
 def test_weights_of_a_query_sum_to_one():
     """Over all keys of a head the weights of its G T queries sum to G T."""
     x = make(1, 1, 8, 2, 500, 128, 2000, torch.bfloat16, [1999], True)
