@@ -515,13 +515,18 @@ def psa_decode(q, k_cache=None, v_cache=None, cache_len=None, k_prefix=None, v_p
             _arg("prefix_len", prefix_len, q, (Bp,), torch.int32), _arg("k_cache", k_cache, q, own, q.dtype),
             _arg("v_cache", v_cache, q, own, q.dtype), _arg("cache_len", cache_len, q, (B,), torch.int32))
     ws = _serve_ws(ws, psa_decode_workspace_size(B, Hq, Hkv, T, d, Bp, P, C), q)
+    at_q = _arg("q", q, q, q.shape, q.dtype)
     if out is None:
-        out = torch.empty_like(q)
+        out = torch.empty_like(q)   # (new buffers need no check)
+        at_out = out.data_ptr()
+    else:
+        at_out = _arg("out", out, q, q.shape, q.dtype)
     if lse is None and want_lse:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
-    _serve("psa_decode", q, _arg("q", q, q, (B, Hq, T, d), q.dtype), *args, B, Hq, Hkv, T, d, Bp, P, C, dt,
-           _arg("out", out, q, (B, Hq, T, d), q.dtype), _arg("lse", lse, q, (B, Hq, T), torch.float32),
-           ws.data_ptr(), ws.numel())
+        lse = torch.empty(B, Hq, T, dtype=torch.float32, device=q.device)
+        at_lse = lse.data_ptr()
+    else:
+        at_lse = _arg("lse", lse, q, (B, Hq, T), torch.float32)
+    _serve("psa_decode", q, at_q, *args, B, Hq, Hkv, T, d, Bp, P, C, dt, at_out, at_lse, ws.data_ptr(), ws.numel())
     return (out, lse) if lse is not None else out
 
 
@@ -551,14 +556,16 @@ def psa_key_weight(q, k, lse, key_len=None, causal: bool = False, score=None, ws
     if lse is None:
         raise ValueError("lse (float32 [B, Hq, T]) of the queries is required")
     slots = (Bk, Hkv, C)
-    args = (_arg("q", q, q, (B, Hq, T, d), q.dtype), _arg("k", k, q, (Bk, Hkv, C, d), q.dtype),
+    args = (_arg("q", q, q, q.shape, q.dtype), _arg("k", k, q, (Bk, Hkv, C, d), q.dtype),
             _arg("lse", lse, q, (B, Hq, T), torch.float32), _arg("key_len", key_len, q, (Bk,), torch.int32),
             _arg("score", score, q, slots, torch.float32))
     ws = _serve_ws(ws, psa_key_weight_workspace_size(B, Hq, Hkv, T, d, Bk, C), q)
     if out is None:
-        out = torch.empty(slots, dtype=torch.float32, device=q.device)
-    _serve("psa_key_weight", q, *args, B, Hq, Hkv, T, d, Bk, C, int(causal), dt,
-           _arg("out", out, q, slots, torch.float32), ws.data_ptr(), ws.numel())
+        out = torch.empty(Bk, Hkv, C, dtype=torch.float32, device=q.device)
+        at_out = out.data_ptr()
+    else:
+        at_out = _arg("out", out, q, slots, torch.float32)
+    _serve("psa_key_weight", q, *args, B, Hq, Hkv, T, d, Bk, C, int(causal), dt, at_out, ws.data_ptr(), ws.numel())
     return out
 
 
@@ -589,25 +596,31 @@ def psa_cache_evict(k, v, score, budget: int, pos=None, cache_len=None, sink: in
     _dtype16("k", k)
     need = psa_cache_evict_workspace_size(B, Hkv, C, budget)
     full = (B, Hkv, C, d)
-    args = (_arg("k", k, k, full, k.dtype), _arg("v", v, k, full, k.dtype),
-            _arg("score", score, k, (B, Hkv, C), torch.float32), _arg("pos", pos, k, (B, Hkv, C), torch.int32),
-            _arg("cache_len", cache_len, k, (B,), torch.int32))
+    at_k, at_v = _arg("k", k, k, full, k.dtype), _arg("v", v, k, full, k.dtype)
+    at_score = _arg("score", score, k, (B, Hkv, C), torch.float32)
+    at_pos = _arg("pos", pos, k, (B, Hkv, C), torch.int32)
+    at_len = _arg("cache_len", cache_len, k, (B,), torch.int32)
     ws = _serve_ws(ws, need, k)
     if out is None:
         if need == 0:
             raise PSAError("psa_cache_evict", PSA_ERR_ARG if budget <= 0 else PSA_ERR_SHAPE)
-        new = lambda *s, dtype: torch.empty(s, dtype=dtype, device=k.device)  # noqa: E731
+        new = lambda *s, dtype: torch.empty(*s, dtype=dtype, device=k.device)  # noqa: E731
         out = (new(B, Hkv, budget, d, dtype=k.dtype), new(B, Hkv, budget, d, dtype=k.dtype),
                new(B, Hkv, budget, dtype=torch.float32), new(B, Hkv, budget, dtype=torch.int32),
                new(B, dtype=torch.int32), new(B, Hkv, budget, dtype=torch.int32))
     k_out, v_out, score_out, pos_out, len_out, kept = out
-    C_out = _shape4("k_out", k_out)[2]
-    rows, slots = (B, Hkv, C_out, d), (B, Hkv, C_out)
-    _serve("psa_cache_evict", k, *args, B, Hkv, C, d, budget, sink, recent, C_out,
-           _arg("k_out", k_out, k, rows, k.dtype), _arg("v_out", v_out, k, rows, k.dtype),
-           _arg("score_out", score_out, k, slots, torch.float32), _arg("pos_out", pos_out, k, slots, torch.int32),
-           _arg("len_out", len_out, k, (B,), torch.int32), _arg("kept", kept, k, (B, Hkv, budget), torch.int32),
-           ws.data_ptr(), ws.numel())
+    # (in place: the inputs, which are checked)
+    if k_out is k and v_out is v and score_out is score:
+        C_out, slots, outs = C, (B, Hkv, C), (at_k, at_v, at_score)
+    else:
+        C_out = _shape4("k_out", k_out)[2]
+        rows, slots = (B, Hkv, C_out, d), (B, Hkv, C_out)
+        outs = (_arg("k_out", k_out, k, rows, k.dtype), _arg("v_out", v_out, k, rows, k.dtype),
+                _arg("score_out", score_out, k, slots, torch.float32))
+    _serve("psa_cache_evict", k, at_k, at_v, at_score, at_pos, at_len, B, Hkv, C, d, budget, sink, recent, C_out, *outs,
+           at_pos if pos_out is pos and C_out == C else _arg("pos_out", pos_out, k, slots, torch.int32),
+           at_len if len_out is cache_len else _arg("len_out", len_out, k, (B,), torch.int32),
+           _arg("kept", kept, k, (B, Hkv, budget), torch.int32), ws.data_ptr(), ws.numel())
     return k_out, v_out, score_out, pos_out, len_out, kept
 
 
