@@ -157,3 +157,78 @@ def test_offsets_past_32_bits():
     got = psa.psa_cache_evict(k, v, score, 2)
     assert (got[5] == torch.tensor([7, C - 1], dtype=torch.int32, device="cuda")).all()
     assert (got[0][:, :, 1] == 3.0).all() and torch.equal(got[0][:, :, 0], k[:, :, 7])
+
+
+def test_a_captured_step_equals_the_eager_one():
+    """Append, attend, add weights, evict: one graph, replayed as the lengths
+    on the device grow to the budget and stay there."""
+    B, H, G, d, budget, steps = 3, 2, 4, 128, 20, 9
+    C = budget + 1
+    g = torch.Generator().manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=g).bfloat16().cuda()  # noqa: E731
+    tokens = [(r(B, H * G, 1, d), r(B, H, 1, d), r(B, H, 1, d)) for _ in range(steps)]
+    start = [r(B, H, C, d), r(B, H, C, d), torch.rand(B, H, C, generator=g).cuda(),
+             torch.arange(C, dtype=torch.int32).expand(B, H, C).contiguous().cuda(),
+             torch.tensor([budget, budget - 3, 0], dtype=torch.int32).cuda()]
+    spaces = (psa.decode_workspace(B, H * G, H, 1, d, C=C), psa.key_weight_workspace(B, H * G, H, 1, d, B, C),
+              psa.cache_evict_workspace(B, H, C, budget))
+
+    def step(state, q, k, v, out, lse, kept):
+        kc, vc, sc, pos, n = state
+        slot = n.long()[:, None, None, None].expand(B, H, 1, d)
+        kc.scatter_(2, slot, k)
+        vc.scatter_(2, slot, v)
+        sc.scatter_(2, slot[..., 0], 0.0)
+        pos.scatter_(2, slot[..., 0], pos.amax(-1, keepdim=True) + 1)
+        n += 1
+        psa.psa_decode(q, kc, vc, n, ws=spaces[0], out=out, lse=lse)
+        psa.psa_key_weight(q, kc, lse, n, causal=True, score=sc, ws=spaces[1], out=sc)
+        psa.psa_cache_evict(kc, vc, sc, budget, pos=pos, cache_len=n, sink=1, recent=4, ws=spaces[2],
+                            out=(kc, vc, sc, pos, n, kept))
+
+    outs = lambda: (torch.empty_like(tokens[0][0]), torch.empty(B, H * G, 1, device="cuda"),  # noqa: E731
+                    torch.empty(B, H, budget, dtype=torch.int32, device="cuda"))
+    eager, want = [t.clone() for t in start], []
+    for t in tokens:
+        o = outs()
+        step(eager, *t, *o)
+        want.append([x.clone() for x in (*o, *eager)])
+    state, io, o = [t.clone() for t in start], [t.clone() for t in tokens[0]], outs()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(state, *io, *o)
+    for t, w in zip(tokens, want):
+        for x, y in zip(io, t):
+            x.copy_(y)
+        graph.replay()
+        assert all(torch.equal(x, y) for x, y in zip((*o, *state), w))
+    assert state[-1].tolist() == [budget, budget, min(budget, steps)]
+    assert all(psa.psa_read_status(w) == psa.PSA_OK for w in spaces)
+
+
+def test_two_streams_with_their_own_workspaces():
+    """The same calls on two streams at once, interleaved, give what they give alone."""
+    g = torch.Generator().manual_seed(4)
+    r = lambda *s: torch.randn(*s, generator=g).half().cuda()  # noqa: E731
+    B, H, G, T, d, C = 6, 2, 3, 40, 64, 3000
+    q, k, v = r(B, H * G, T, d), r(B, H, C, d), r(B, H, C, d)
+    n = torch.tensor([3000, 40, 2999, 128, 1000, 77], dtype=torch.int32, device="cuda")
+
+    def run(stream=None):
+        out, lse = psa.psa_decode(q, k, v, n, want_lse=True, stream=stream)
+        score = psa.psa_key_weight(q, k, lse, n, causal=True, stream=stream)
+        return (out, lse, score, *psa.psa_cache_evict(k, v, score, 1000, cache_len=n, recent=50, stream=stream))
+
+    alone = run()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    both = [[run(s) for s in streams] for _ in range(4)]
+    torch.cuda.synchronize()
+    there = alone[8] >= 0
+    for pair in both:
+        for got in pair:
+            for i in (0, 1, 2, 7, 8):
+                assert torch.equal(got[i], alone[i])
+            for i in (3, 4, 5, 6):   # (slots past a length are left as they were)
+                assert torch.equal(got[i][there], alone[i][there])
