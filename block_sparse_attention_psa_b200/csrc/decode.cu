@@ -41,10 +41,10 @@
 //    that are masked.
 // Measured on one B200 (device time, a call in a stream of calls; floors from
 // 6.54 TB/s and 1658 TFLOP/s): 64 ragged caches of up to 4096, 8 KV heads of 4
-// query heads, d = 128: 95 us, 5.8 TB/s (floor 85). 16 samples of a 32K prompt:
-// 43 us (23): 22 us of streaming at the DRAM's rate, the rest is the schedule
+// query heads, d = 128: 93 us, 5.9 TB/s (floor 85). 16 samples of a 32K prompt:
+// 42 us (23): 22 us of streaming at the DRAM's rate, the rest is the schedule
 // (1.7), the first load (3), the last tile's chain (5), the imbalance of the
-// SMs (4) and the join (7). 64 sequences of 64 heads over a 128K prefix: 282 to
+// SMs (4) and the join (5). 64 sequences of 64 heads over a 128K prefix: 282 to
 // 300 us, 920 to 980 TFLOP/s (166): a pair of items takes ~3280 cycles, set by
 // one stream's chain S -> softmax (2030: 128 exponentials of a thread alone are
 // 1024) -> PV -> S, the tensor core working 2048 of them, under the power cap
@@ -778,15 +778,31 @@ __device__ __forceinline__ int part_at(const RowParts& k, int q) {
 }
 
 template <int kV>
-__device__ __forceinline__ void add_part(float (&acc)[kV], float f, const float* src) {
+__device__ __forceinline__ void load_part(float (&v)[kV], const float* src) {
   if constexpr (kV == 4) {
-    const float4 v = *reinterpret_cast<const float4*>(src);
-    acc[0] += f * v.x, acc[1] += f * v.y, acc[2] += f * v.z, acc[3] += f * v.w;
+    const float4 u = *reinterpret_cast<const float4*>(src);
+    v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
   } else {
-    const float2 v = *reinterpret_cast<const float2*>(src);
-    acc[0] += f * v.x, acc[1] += f * v.y;
+    const float2 u = *reinterpret_cast<const float2*>(src);
+    v[0] = u.x, v[1] = u.y;
   }
 }
+template <int kV>
+__device__ __forceinline__ void add_part(float (&acc)[kV], float f, const float (&v)[kV]) {
+#pragma unroll
+  for (int i = 0; i < kV; ++i) acc[i] += f * v[i];
+}
+template <int kV>
+__device__ __forceinline__ void add_part(float (&acc)[kV], float f, const float* src) {
+  float v[kV];
+  load_part<kV>(v, src);
+  add_part<kV>(acc, f, v);
+}
+// O of a warp's first parts is fetched along with the references, before it is
+// known which parts count (a part that does not is not added, whatever is
+// there).  A round trip less: 16 samples of a 32K prompt 43.6 -> 42.6 us a call
+// with four, 41.6 with eight (five of a warp's parts there).
+constexpr int kAhead = 8;
 
 // Few parts per row: a warp per row, 32 parts at a time.  (4096 rows of 14
 // parts: 22 us with a block of eight warps per row, whose barriers and waves
@@ -805,6 +821,10 @@ __global__ void __launch_bounds__(128) merge_kernel(const Params p, int rows, ui
 #pragma unroll
   for (int i = 0; i < kV; ++i) acc[i] = 0.f;
   float M = -INFINITY, L = 0.f;
+  float ahead[kAhead][kV];
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j)
+    if (j < n) load_part<kV>(ahead[j], p.part_o + static_cast<long long>(part_at(k, j)) * D + lane * kV);
   for (int q0 = 0; q0 < n; q0 += 32) {
     const int at = q0 + lane < n ? part_at(k, q0 + lane) : 0;
     const float2 ml = q0 + lane < n ? p.part_ml[at] : make_float2(-INFINITY, 0.f);
@@ -823,8 +843,15 @@ __global__ void __launch_bounds__(128) merge_kernel(const Params p, int rows, ui
 #pragma unroll
     for (int i = 0; i < kV; ++i) acc[i] *= old;
     const int m = min(32, n - q0);
+    if (q0 == 0) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const float fj = __shfl_sync(0xffffffffu, f, j);  // (0 from n on)
+        if (fj != 0.f) add_part<kV>(acc, fj, ahead[j]);
+      }
+    }
 #pragma unroll 8
-    for (int j = 0; j < m; ++j) {
+    for (int j = q0 == 0 ? kAhead : 0; j < m; ++j) {
       const float fj = __shfl_sync(0xffffffffu, f, j);
       const int aj = __shfl_sync(0xffffffffu, at, j);
       if (fj != 0.f) add_part<kV>(acc, fj, p.part_o + static_cast<long long>(aj) * D + lane * kV);
@@ -861,6 +888,11 @@ __global__ void __launch_bounds__(256) merge_wide_kernel(const Params p, uint16_
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const RowParts k = row_parts(p, row);
   const int n = uniform(k.cnt[0] + k.cnt[1]);
+  float ahead[kAhead][kV];
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j)
+    if (warp + W * j < n)
+      load_part<kV>(ahead[j], p.part_o + static_cast<long long>(part_at(k, warp + W * j)) * D + lane * kV);
   float M = -INFINITY;
   for (int q = threadIdx.x; q < n; q += 32 * W) {
     const int a = part_at(k, q);
@@ -894,8 +926,13 @@ __global__ void __launch_bounds__(256) merge_wide_kernel(const Params p, uint16_
   float acc[kV];
 #pragma unroll
   for (int i = 0; i < kV; ++i) acc[i] = 0.f;
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) {
+    const float f = warp + W * j < n ? w[warp + W * j] : 0.f;
+    if (f != 0.f) add_part<kV>(acc, f, ahead[j]);
+  }
 #pragma unroll 4
-  for (int q = warp; q < n; q += W) {
+  for (int q = warp + W * kAhead; q < n; q += W) {
     const float f = w[q];
     if (f != 0.f) add_part<kV>(acc, f, p.part_o + static_cast<long long>(at[q]) * D + lane * kV);
   }
