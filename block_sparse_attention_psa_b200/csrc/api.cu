@@ -743,7 +743,7 @@ int psa_cache_evict(const void* k, const void* v, const float* score, const int*
   a.kept = kept;
   a.status = reinterpret_cast<int*>(ws);
   a.nk = reinterpret_cast<int*>(ws + 256);
-  a.late = reinterpret_cast<int*>(ws + 256 + round256(static_cast<size_t>(B) * 4));
+  a.holes = reinterpret_cast<int*>(ws + 256 + round256(static_cast<size_t>(B) * 4));
   return cuda_status(psa::launch_evict(a, static_cast<cudaStream_t>(stream)));
 }
 

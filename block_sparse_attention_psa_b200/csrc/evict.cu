@@ -19,13 +19,14 @@
 // ranks are combined through distributed shared memory, a few words per CTA
 // (sums of 64 bins first, then one group's bins).  Scores and positions are
 // read from DRAM once.  Every warp owns a contiguous run of slots for the tie
-// ranks; holes and survivors are ranked from one bit per slot, a word per thread.
+// ranks; holes and survivors are ranked from one bit per slot, a word per thread,
+// and a survivor finds its hole's slot in the shared memory of the CTA that has it.
 // move_kernel is a gather of 2d-byte rows: 16 bytes per lane, K and V rows of
 // several slots in flight per warp; bound by DRAM.
 // Measured on one B200 (device time): 32 caches of up to 5001 entries down to
-// 4096, 8 heads, d = 128: 154 us, 5.9 TB/s (floor 139); a 128K prefill down to
-// 16384: 54 us (22), about half of it the selection (two radix rounds of 4 us,
-// the keys 6, ranks and lists 8); one entry of 1025: 12 us, all latency.
+// 4096, 8 heads, d = 128: 152 us, 6.0 TB/s (floor 139); a 128K prefill down to
+// 16384: 53 us (22), about half of it the selection (two radix rounds of 4 us,
+// the keys 6, ranks and lists 7); one entry of 1025: 5.6 us, all latency.
 #include <climits>
 #include <cooperative_groups.h>
 
@@ -46,7 +47,7 @@ struct SelectParams {
   const int* pos;        // null: the slot index
   const int* cache_len;  // null: C
   int* kept;             // [B * Hkv][budget]
-  int* late;             // scratch [B * Hkv][budget]: survivors from slot nk on, ascending
+  int* holes;            // scratch [B * Hkv][budget] where the keys are not on chip: the holes, ascending
   int* nk_out;           // scratch [B]
   int* status;
   int B, Hkv, C, budget, sink, recent;
@@ -87,7 +88,7 @@ __device__ __forceinline__ int2 warps_exclusive(int2* buf, int2 mine, int2& tota
 struct SelectShared {
   uint32_t hist[3][kBins];  // one per round: nothing is cleared while it may still be read
   uint32_t coarse[3][32];   // sums of 64 bins
-  int2 count[2];            // totals of a CTA, one per exchange
+  int2 count[2];            // totals of a CTA (or its lowest key and slot), one per exchange
   int last;                 // latest position
 };
 
@@ -99,6 +100,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) select_kernel(const SelectPara
   __shared__ __align__(16) SelectShared sh;
   __shared__ int2 buf[33];
   __shared__ uint32_t pick[3];  // chosen bin, keys above it, keys in it
+  __shared__ int hole_count[8]; // of each CTA
   cg::cluster_group cl = cg::this_cluster();
   const int rank = CL ? static_cast<int>(cl.block_rank()) : 0;
   const int ncta = CL ? static_cast<int>(cl.num_blocks()) : 1;
@@ -137,7 +139,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1) select_kernel(const SelectPara
   const int nk = min(len, p.budget);
   if (rank == 0 && bh % p.Hkv == 0 && tid == 0) p.nk_out[b] = nk;
   int* kept = p.kept + static_cast<long long>(bh) * p.budget;
-  int* late = p.late + static_cast<long long>(bh) * p.budget;
   const float* score = p.score + static_cast<long long>(bh) * p.C;
   const int* pos = p.pos ? p.pos + static_cast<long long>(bh) * p.C : nullptr;
 
@@ -200,6 +201,45 @@ __global__ void __launch_bounds__(kMaxThreads, 1) select_kernel(const SelectPara
     for (int i = max(s1 - s0, 0) + tid; i < p.slice; i += nthr) keys[i] = 0u;
   auto key = [&](int i) -> uint32_t { return p.keys_on_chip ? keys[i - s0] : (i < s1 ? make_key(i) : 0u); };
   __syncthreads();
+
+  if (len - nk == 1) {
+    // ---- one entry goes (a decode step at its budget): the lowest key, of
+    // equal ones the last; slot nk takes its place.  One reduction instead of
+    // three rounds and the ranks: a call on 1025 entries 11.7 -> 5.6 us.
+    uint32_t hi = 0xffffffffu, lo = 0xffffffffu;  // key, ~slot
+#pragma unroll 4
+    for (int i = s0 + tid; i < s1; i += nthr) {
+      const uint32_t k = key(i);
+      if (k <= hi) hi = k, lo = ~static_cast<uint32_t>(i);
+    }
+    __syncwarp();
+    auto lowest = [&]() {
+      const uint32_t k = __reduce_min_sync(0xffffffffu, hi);
+      lo = __reduce_min_sync(0xffffffffu, hi == k ? lo : 0xffffffffu);
+      hi = k;
+    };
+    auto give = [&](int2 v, bool there) {
+      hi = there ? static_cast<uint32_t>(v.x) : 0xffffffffu;
+      lo = there ? static_cast<uint32_t>(v.y) : 0xffffffffu;
+    };
+    lowest();
+    if (lane == 0) buf[warp] = make_int2(static_cast<int>(hi), static_cast<int>(lo));
+    __syncthreads();
+    __syncwarp();
+    give(lane < (nthr >> 5) ? buf[lane] : make_int2(0, 0), lane < (nthr >> 5));
+    lowest();
+    if constexpr (CL) {
+      if (tid == 0) sh.count[0] = make_int2(static_cast<int>(hi), static_cast<int>(lo));
+      cl.sync();
+      __syncwarp();
+      give(lane < ncta ? peer(lane)->count[0] : make_int2(0, 0), lane < ncta);
+      lowest();
+    }
+    const int gone = static_cast<int>(~lo);
+    for (int i = s0 + tid; i < min(s1, nk); i += nthr) kept[i] = i == gone ? nk : i;
+    if constexpr (CL) cl.sync();  // the others' shared memory has been read
+    return;
+  }
 
   // ---- radix select of the nk-th largest key
   // After a round whose bin is needed whole, the bits so far decide.
@@ -372,6 +412,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) select_kernel(const SelectPara
   if constexpr (CL) {
     if (tid == 0) sh.count[1] = base;
     cl.sync();
+    if (tid < ncta) hole_count[tid] = peer(tid)->count[1].x;
     for (int r = 0; r < rank; ++r) {
       const int2 c = peer(r)->count[1];
       first.x += c.x;
@@ -380,21 +421,38 @@ __global__ void __launch_bounds__(kMaxThreads, 1) select_kernel(const SelectPara
   } else {
     __syncthreads();
   }
+  // The holes' slots, ascending, take the keys' place (all of them are read).
+  int* holes = p.holes + static_cast<long long>(bh) * p.budget;
+  int* mine = p.keys_on_chip ? reinterpret_cast<int*>(keys) : holes + first.x;
 #pragma unroll 2
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const int w = (i0 - s0) >> 5;
-    const uint32_t word = stay[w], early = below(nk, i0), bit = 1u << lane;
-    const uint32_t far = word & ~early;
-    if (far & bit) late[first.y + rank_at[w].y + __popc(far & (bit - 1u))] = i0 + lane;
-    if (word & early & bit) kept[i0 + lane] = i0 + lane;
-  }
-  sync_all();  // orders the list's global writes; nobody reads another's shared memory after it
-#pragma unroll 4
   for (int i0 = w0; i0 < min(w1, nk); i0 += 32) {
     const int w = (i0 - s0) >> 5;
-    const uint32_t open = below(min(nk, w1), i0) & ~stay[w], bit = 1u << lane;
-    if (open & bit) kept[i0 + lane] = __ldcg(late + first.x + rank_at[w].x + __popc(open & (bit - 1u)));
+    const uint32_t word = stay[w], early = below(min(nk, w1), i0), bit = 1u << lane;
+    const uint32_t open = early & ~word;
+    if (open & bit) mine[rank_at[w].x + __popc(open & (bit - 1u))] = i0 + lane;
+    if (word & early & bit) kept[i0 + lane] = i0 + lane;
   }
+  sync_all();
+  // the r-th late survivor goes to the r-th hole
+#pragma unroll 2
+  for (int i0 = max(w0, nk & ~31); i0 < w1; i0 += 32) {
+    const int w = (i0 - s0) >> 5;
+    const uint32_t far = stay[w] & ~below(nk, i0), bit = 1u << lane;
+    if (far & bit) {
+      int at = first.y + rank_at[w].y + __popc(far & (bit - 1u));
+      if (!p.keys_on_chip) {
+        at = __ldcg(holes + at);
+      } else if constexpr (CL) {
+        int r = 0;
+        for (; r < ncta - 1 && at >= hole_count[r]; ++r) at -= hole_count[r];
+        at = cl.map_shared_rank(mine, r)[at];
+      } else {
+        at = mine[at];
+      }
+      kept[at] = i0 + lane;
+    }
+  }
+  if constexpr (CL) cl.sync();  // the others' shared memory has been read
 }
 
 struct MoveParams {
@@ -471,7 +529,7 @@ cudaError_t launch_evict(const EvictLaunch& a, cudaStream_t st) {
   s.pos = a.pos;
   s.cache_len = a.cache_len;
   s.kept = a.kept;
-  s.late = a.late;
+  s.holes = a.holes;
   s.nk_out = a.nk;
   s.status = a.status;
   s.B = a.B;

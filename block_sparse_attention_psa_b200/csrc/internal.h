@@ -216,7 +216,7 @@ struct EvictLaunch {
   int* kept;            // [B, Hkv, budget]
   int* status;          // workspace: status word,
   int* nk;              // [B],
-  int* late;            // [B, Hkv, budget]
+  int* holes;            // [B, Hkv, budget]
 };
 cudaError_t launch_evict(const EvictLaunch& a, cudaStream_t st);
 

@@ -123,6 +123,16 @@ def test_evicting_one_entry_moves_one_row():
     assert got[5].flatten().tolist() == want
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("C, sink, recent", [(3, 1, 1), (700, 300, 399), (50000, 4, 40000), (300000, 4, 100)])
+def test_one_entry_over_the_budget(C, sink, recent, in_place):
+    """One reduction picks it: over one CTA, a cluster, and keys that do not
+    fit on chip; among few unprotected entries; of equal scores the last."""
+    for kind in ("tails", "equal", "few"):
+        check(make(2, 1, C, 64, kind=kind), [C, C - 1], C - 1, sink, recent, True, in_place)
+        check(make(1, 2, C, 64, kind=kind), [C], C - 1, sink, recent, False, in_place)
+
+
 def test_bad_lengths_are_clamped_and_reported():
     x = make(2, 1, 70, 64)
     ws = psa.cache_evict_workspace(2, 1, 70, 50)
