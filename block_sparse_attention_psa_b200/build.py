@@ -3,6 +3,7 @@
 Usage: ``python -m block_sparse_attention_psa_b200.build [--ptxas-v]``.
 Each ``csrc/*.cu`` is compiled to an object under ``_build/`` (in parallel,
 skipped when up to date) and linked into ``libpsa.so`` next to this file.
+``csrc/call.cpp`` (the binding's serving calls) becomes ``_call.so`` beside it.
 """
 
 from __future__ import annotations
@@ -21,6 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpsa.so")
+CALL = os.path.join(PKG, "_call.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -53,12 +55,41 @@ def _compile(src: str, ptxas_v: bool) -> tuple[str, str]:
     return obj, r.stderr
 
 
+def _build_call() -> str:
+    """The native form of the binding's serving calls, against the PyTorch it
+    is used with (a newer PyTorch builds it anew)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension as ext
+
+    src = os.path.join(CSRC, "call.cpp")
+    newest = max(os.path.getmtime(p) for p in (src, os.path.join(INCLUDE, "psa.h"), torch.__file__))
+    if os.path.exists(CALL) and os.path.getmtime(CALL) >= newest:
+        return CALL
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    inc = [INCLUDE, *ext.include_paths(), os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = f"{CALL}.{os.getpid()}"   # a process that has the old one mapped keeps it
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *(f"-isystem{p}" for p in inc), src,
+           "-o", tmp, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALL)
+    return CALL
+
+
 def build(ptxas_v: bool = False, verbose: bool = False) -> str:
-    """Compile every CUDA source for sm_100a and link ``libpsa.so``."""
+    """Compile every CUDA source for sm_100a and link ``libpsa.so``, and the
+    binding's ``_call.so``."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        call = ex.submit(_build_call)
         results = list(ex.map(lambda s: _compile(s, ptxas_v), srcs))
+        call.result()
     objs = [o for o, _ in results]
     if verbose or ptxas_v:
         for _, log in results:

@@ -7,6 +7,11 @@ call is issued with the device of its main tensor current, on that device's
 ``torch.cuda.current_stream()`` unless a stream is given.
 A non-zero status raises :class:`PSAError`.  There is no fallback: if the
 library is missing, :func:`lib` raises.
+
+The serving calls, whose kernels may take less time than reading their
+arguments in Python, go through ``_call.so`` (``csrc/call.cpp``) where it is
+built: it makes the same call for arguments that are plainly right, and leaves
+all others, and every error, to the functions here.
 """
 
 from __future__ import annotations
@@ -16,6 +21,11 @@ import functools
 import os
 
 import torch
+
+try:
+    from . import _call as _native
+except ImportError:   # not built for this PyTorch: the same calls, some 10 us slower on the host
+    _native = None
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpsa.so")
@@ -92,6 +102,10 @@ def lib() -> ctypes.CDLL:
                                "`python -m block_sparse_attention_psa_b200.build`")
         L = ctypes.CDLL(LIB_PATH)
         _declare(L)
+        if _native is not None:
+            _native.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                L.psa_decode, L.psa_decode_workspace_size, L.psa_key_weight, L.psa_key_weight_workspace_size,
+                L.psa_cache_evict, L.psa_cache_evict_workspace_size)))
         _lib = L
     return _lib
 
@@ -492,6 +506,10 @@ def psa_decode(q, k_cache=None, v_cache=None, cache_len=None, k_prefix=None, v_p
     if stream is not None:   # what is allocated here then belongs to that stream
         with torch.cuda.stream(stream):
             return psa_decode(q, k_cache, v_cache, cache_len, k_prefix, v_prefix, prefix_len, ws, out, lse, want_lse)
+    if _native is not None:
+        r = _native.decode(q, k_cache, v_cache, cache_len, k_prefix, v_prefix, prefix_len, ws, out, lse, want_lse)
+        if r is not None:
+            return r
     B, Hq, T, d = _shape4("q", q)
     dt = _dtype16("q", q)
     if k_cache is None and k_prefix is None:
@@ -550,6 +568,10 @@ def psa_key_weight(q, k, lse, key_len=None, causal: bool = False, score=None, ws
     if stream is not None:
         with torch.cuda.stream(stream):
             return psa_key_weight(q, k, lse, key_len, causal, score, ws, out)
+    if _native is not None:
+        r = _native.key_weight(q, k, lse, key_len, causal, score, ws, out)
+        if r is not None:
+            return r
     B, Hq, T, d = _shape4("q", q)
     dt = _dtype16("q", q)
     Bk, Hkv, C, _ = _shape4("k", k)
@@ -592,6 +614,10 @@ def psa_cache_evict(k, v, score, budget: int, pos=None, cache_len=None, sink: in
     if stream is not None:
         with torch.cuda.stream(stream):
             return psa_cache_evict(k, v, score, budget, pos, cache_len, sink, recent, ws, out)
+    if _native is not None:
+        r = _native.cache_evict(k, v, score, budget, pos, cache_len, sink, recent, ws, out)
+        if r is not None:
+            return r
     B, Hkv, C, d = _shape4("k", k)
     _dtype16("k", k)
     need = psa_cache_evict_workspace_size(B, Hkv, C, budget)

@@ -232,3 +232,70 @@ def test_two_streams_with_their_own_workspaces():
                 assert torch.equal(got[i], alone[i])
             for i in (3, 4, 5, 6):   # (slots past a length are left as they were)
                 assert torch.equal(got[i][there], alone[i][there])
+
+
+def test_the_native_calls_are_the_python_ones(monkeypatch):
+    """_call.so makes the calls here (not the Python form), with the same results."""
+    assert psa._native is not None
+    psa.lib()
+    g = torch.Generator().manual_seed(6)
+    r = lambda *s: torch.randn(*s, generator=g).bfloat16().cuda()  # noqa: E731
+    B, H, G, T, d, P, C = 4, 2, 3, 2, 64, 300, 200
+    q, kp, vp, k, v = r(B, H * G, T, d), r(2, H, P, d), r(2, H, P, d), r(B, H, C, d), r(B, H, C, d)
+    n = torch.tensor([200, 3, 0, 77], dtype=torch.int32, device="cuda")
+    m = torch.tensor([300, 129], dtype=torch.int32, device="cuda")
+    pos = torch.arange(C, dtype=torch.int32, device="cuda").expand(B, H, C).contiguous()
+
+    def run(given):
+        ws = dict(ws=psa.decode_workspace(B, H * G, H, T, d, 2, P, C)) if given else {}
+        out, lse = psa.psa_decode(q, k, v, n, kp, vp, m, want_lse=True, **ws)
+        a = [out, lse, psa.psa_decode(q, k, v, n), psa.psa_decode(q, k_prefix=kp, v_prefix=vp)]
+        score = psa.psa_key_weight(q, k, lse, n, causal=True)
+        a += [score, psa.psa_key_weight(q, kp, lse, m)]
+        if given:
+            out = torch.empty_like(q)
+            assert psa.psa_decode(q, k, v, n, out=out) is out
+            assert psa.psa_key_weight(q, k, lse, n, score=score, out=score) is score
+            a += [out, score.clone()]
+            bufs = (k.clone(), v.clone(), score, pos.clone(), n.clone(),
+                    torch.empty(B, H, 50, dtype=torch.int32, device="cuda"))
+            got = psa.psa_cache_evict(*bufs[:3], 50, pos=bufs[3], cache_len=bufs[4], sink=2, recent=9, out=bufs)
+            assert all(x is y for x, y in zip(got, bufs))
+        else:
+            got = psa.psa_cache_evict(k, v, score, 50, cache_len=n, recent=9)
+        kept = got[5] >= 0
+        return a + [t[:, :, :50][kept] for t in got[:4]] + [got[4], got[5]]
+
+    for given in (False, True):
+        native = run(given)
+        with monkeypatch.context() as mp:
+            mp.setattr(psa, "_native", None)
+            python = run(given)
+        assert len(native) == len(python) and all(torch.equal(x, y) for x, y in zip(native, python))
+
+
+def test_what_the_native_calls_leave_to_python_is_refused():
+    g = torch.Generator().manual_seed(7)
+    q, k, v = (torch.randn(2, 2, 8, 64, generator=g).bfloat16().cuda() for _ in range(3))
+    n = torch.tensor([8, 5], dtype=torch.int32, device="cuda")
+    out, lse = psa.psa_decode(q, k, v, n, want_lse=True)
+    score = psa.psa_key_weight(q, k, lse, n)
+    small = torch.empty(256, dtype=torch.uint8, device="cuda")
+    for bad in (dict(k_cache=k.half()), dict(cache_len=n.long()), dict(cache_len=n[:1]), dict(v_cache=v[:, :, :4]),
+                dict(v_cache=v.transpose(1, 2)), dict(k_cache=k.cpu()), dict(ws=small), dict(lse=lse[:1]),
+                dict(out=out.float()), dict(v_cache=None), dict(q=q.float()), dict(q=q[0]), dict(q=None),
+                dict(prefix_len=n)):
+        with pytest.raises((ValueError, AttributeError)):
+            psa.psa_decode(**{**dict(q=q, k_cache=k, v_cache=v, cache_len=n), **bad})
+    for bad in (dict(out=k), dict(out=q[:, :, :4])):
+        with pytest.raises((ValueError, psa.PSAError)):
+            psa.psa_decode(**{**dict(q=q, k_cache=k, v_cache=v, cache_len=n), **bad})
+    for bad in (dict(lse=None), dict(lse=lse.half()), dict(key_len=n.cpu()), dict(score=score[..., :4]),
+                dict(out=score.double()), dict(k=k[:1]), dict(ws=small[:10])):
+        with pytest.raises((ValueError, psa.PSAError)):
+            psa.psa_key_weight(**{**dict(q=q, k=k, lse=lse, key_len=n), **bad})
+    for bad in (dict(budget=0), dict(budget=9), dict(sink=3, recent=2), dict(pos=n), dict(score=score.half()),
+                dict(out=(k, v, score, None, n, n)), dict(out=(k, v.clone(), score, n, n, n))):
+        with pytest.raises((ValueError, psa.PSAError)):
+            psa.psa_cache_evict(**{**dict(k=k, v=v, score=score, budget=4, cache_len=n), **bad})
+    assert torch.equal(out, psa.psa_decode(q, k, v, n))
