@@ -59,6 +59,7 @@
 // hand-overs between tiles, and 2100 of 6100 between units of two tiles.
 // Every wait is bounded.
 #include <climits>
+#include <cmath>
 
 #include "internal.h"
 #include "sm100.cuh"
@@ -918,11 +919,25 @@ bool make_plan(Params& p, int B, int G, int Hkv, int T, int Bk, int C) {
   p.N = (p.nb * p.rb + 15) & ~15;
   p.pairs = (C + 255) / 256;
   const long long units = static_cast<long long>(Bk) * Hkv * p.pairs;
-  // two units per SM, of at least four query tiles each, 16 parts at most
-  long long z = (2LL * kPlanSms + units - 1) / units;
-  if (z > tiles / 4) z = tiles / 4;
-  if (z > 16) z = 16;
-  p.Z = z < 1 ? 1 : static_cast<int>(z);
+  // Parts, 16 at most: the split whose last SM is done first, counted in query
+  // tiles, where a unit's start costs one (a prefill's two) and the sum of the
+  // parts two; more parts have to gain 1% of the whole, since they are memory.
+  // Units of one size come in rounds; those of a prefill (T > C / 2: from all
+  // query tiles down to none) even out but for about the longest one's length.
+  // (Us a call, against two units per SM of four query tiles or more: 300
+  // queries of 300 keys, 8 heads of 2 KV heads, 15.5 -> 12.1; 64 of 1000, 16 of
+  // 2, 16.8 -> 12.4; 150 of 4000, 64 of 8, 33.2 -> 30.5; 4096 of 4096, 16 of 8,
+  // 61.0 -> 59.5.)
+  const bool even = !(p.by_head && 2LL * T > C);
+  double least = 0, gain = 0;
+  p.Z = 1;
+  for (int z = 1; z <= 16 && z <= tiles; ++z) {
+    const double rounds = static_cast<double>(units) * z / kPlanSms, each = static_cast<double>(tiles) / z;
+    const double cost =
+        (even ? std::ceil(rounds) * (std::ceil(each) + 1) : rounds * (0.5 * each + 2) + each) + (z > 1 ? 2 : 0);
+    if (z == 1) gain = 0.01 * cost;
+    if (z == 1 || cost < least - gain) least = cost, p.Z = z;
+  }
   p.units = units * p.Z;
   return units <= INT_MAX && static_cast<long long>(Bk) * Hkv * tiles <= INT_MAX;
 }
