@@ -8,10 +8,10 @@
 // operands K-major in shared memory): a thread owns one TMEM lane, i.e. one
 // key, so a key's sum runs inside a thread and needs no exchange.  The lse of
 // the queries runs along the columns and is read from shared memory, four
-// columns per broadcast load; lse_kernel lays it out beforehand as the tiles
-// want it (-lse log2 e, -inf in columns without a query), so that a tile's
-// 128 words come with one bulk copy, with a mark for columns of -inf.  (A warp that gathered them itself was what
-// a 64-token window waited for: 7000 cycles a unit.)
+// columns per broadcast load; a warp of its own gathers it tile by tile (-lse
+// log2 e, -inf in columns without a query, with a mark for columns of -inf), up
+// to four tiles ahead. (Laid out by a kernel of its own beforehand it cost a
+// launch: 48 queries of 1000 keys 14.7 -> 13.5 us, 64 of 128K 109 -> 108.)
 //
 //  * Decode reads K once for few queries: bound by DRAM.  A prefill does 2 d
 //    operations and one exponential per (query, key) pair: an SM's tensor
@@ -96,7 +96,6 @@ struct Params {
   const float* score_in;  // nullable
   float* score_out;
   float* part;            // [Z][Bk * Hkv][C] when Z > 1
-  float* nl;              // [Bk * Hkv][all tiles][kNl]: -lse log2(e)
   int B, G, Hkv, T, Bk, n, C, causal;
   int GT, by_head;        // by_head: query tiles of one head
   int nb, rb;             // query tile: sequences x rows (box)
@@ -175,12 +174,6 @@ struct Tile {
     } else {
       i += p.nb;
     }
-  }
-  // place among all tiles of the KV head
-  __device__ __forceinline__ int index(const Params& p) const {
-    if (p.by_head) return (i * p.G + g) * p.tiles + r0 / 128;
-    if (p.GT >= 128) return i * ((p.GT + 127) / 128) + r0 / 128;
-    return i / p.nb;
   }
 };
 
@@ -261,10 +254,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* q_empty = bars + 8;   // [kQ]
   uint64_t* s_full = bars + 12;   // [2 streams][2] S^T ready        (commit)
   uint64_t* s_empty = bars + 16;  // [2 streams][2] read             (4 warps)
-  uint64_t* l_full = bars + 20;   // [kLse] lse of a query tile      (bulk copy)
+  uint64_t* l_full = bars + 20;   // [kLse] lse of a query tile      (warp 2)
   uint64_t* l_empty = bars + 24;  // [kLse] read                     (16 warps)
   uint64_t* u_full = bars + 28;   // [kRing] a unit published
-  uint64_t* u_empty = bars + 32;  // [kRing] read by loads, MMA issue, 16 warps
+  uint64_t* u_empty = bars + 32;  // [kRing] read by loads, lse, MMA issue, 16 warps
   uint64_t* drain = bars + 36;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc + 320);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -294,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&u_full[i], 1);
-      mbar_init(&u_empty[i], 18);
+      mbar_init(&u_empty[i], 19);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -447,7 +440,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (x.nt < 0 || !ok) break;
         if (x.nt == 0) continue;
         const uint32_t bytes = static_cast<uint32_t>(p.nb * p.rb) * 128 * C::kChunks;
-        const float* nl = p.nl + (static_cast<long long>(x.bk) * p.Hkv + x.hkv) * p.all * kNl;
         for (int pp = 0; ok && pp < x.np; ++pp) {
           const int kb = ku & 1, key0 = x.key0 + 256 * pp;
           if (!(ok = mbar_sleep(&k_empty[kb], ((ku >> 1) & 1) ^ 1, abort_flag, p.status))) break;
@@ -464,11 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           Tile t = {x.i, x.g, x.r0};
           for (int f = 0; f < x.nt; ++f, ++qt) {
             const int st = qt % kQ;
-            const int lt = qt % kLse;
             if (!(ok = mbar_sleep(&q_empty[st], ((qt / kQ) & 1) ^ 1, abort_flag, p.status))) break;
-            if (!(ok = mbar_sleep(&l_empty[lt], ((qt / kLse) & 1) ^ 1, abort_flag, p.status))) break;
-            mbar_arrive_expect_tx(&l_full[lt], kNl * 4);
-            bulk_load(sLse + kNl * lt, nl + static_cast<long long>(t.index(p)) * kNl, kNl * 4, &l_full[lt]);
             mbar_arrive_expect_tx(&q_full[st], bytes);
 #pragma unroll
             for (int ch = 0; ch < C::kChunks; ++ch)
@@ -481,7 +469,70 @@ __global__ void __launch_bounds__(kThreads, 1)
       // no bulk copy may still be writing shared memory when the CTA leaves
       for (int i = max(0, ku - 2); i < ku; ++i) mbar_drain(&k_full[i & 1], (i >> 1) & 1);
       for (int i = max(0, qt - kQ); i < qt; ++i) mbar_drain(&q_full[i % kQ], (i / kQ) & 1);
-      for (int i = max(0, qt - kLse); i < qt; ++i) mbar_drain(&l_full[i % kLse], (i / kLse) & 1);
+    } else if (warp == 2) {
+      // ---------------------------------------------------- lse of the query tiles
+      // -lse log2(e) in the order of the columns, -inf in columns without a
+      // query, four columns a lane; the loads of a tile are under way before
+      // its place is free.
+      int qt = 0, at[4];
+      bool in[4], ok = true;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = 32 * j + lane;
+        if (p.by_head || p.GT >= 128) {
+          at[j] = c;
+          in[j] = true;
+        } else {
+          at[j] = c / p.GT;  // sequence of the tile
+          in[j] = c < p.nb * p.GT;
+        }
+      }
+      while (ok) {
+        Unit x;
+        next_unit(x, false);
+        __syncwarp();
+        const int nt = uniform(x.nt), np = uniform(x.np);
+        if (nt < 0) break;
+        if (lane == 0) mbar_arrive(&u_empty[(nu - 1) % kRing]);
+        __syncwarp();
+        for (int pp = 0; ok && pp < (p.resident ? 1 : np); ++pp) {
+          Tile t = {x.i, x.g, x.r0};
+          for (int f = 0; ok && f < nt; ++f, ++qt) {
+            const int lt = qt % kLse;
+            float* dst = sLse + kNl * lt;
+            float l[4];
+            const long long seq = static_cast<long long>(x.bk) * p.n + t.i;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int c = 32 * j + lane;
+              l[j] = -INFINITY;
+              if (p.by_head) {
+                if (t.r0 + c < p.T)
+                  l[j] = __ldg(p.lse + ((seq * p.Hkv + x.hkv) * p.G + t.g) * p.T + t.r0 + c);
+              } else if (p.GT >= 128) {
+                if (t.r0 + c < p.GT) l[j] = __ldg(p.lse + (seq * p.Hkv + x.hkv) * p.GT + t.r0 + c);
+              } else if (in[j] && t.i + at[j] < p.n) {
+                l[j] = __ldg(p.lse + ((seq + at[j]) * p.Hkv + x.hkv) * p.GT + c - at[j] * p.GT);
+              }
+            }
+            ok = mbar_sleep(&l_empty[lt], ((qt / kLse) & 1) ^ 1, abort_flag, p.status);
+            __syncwarp();
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              // a query that saw nothing (lse -inf) adds nothing
+              const bool none = l[j] == -INFINITY;
+              dst[32 * j + lane] = none ? -INFINITY : -l[j] * kLog2e;
+              const int any = __any_sync(0xffffffffu, none);
+              if (lane == 0) dst[128 + j] = __int_as_float(any);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&l_full[lt]);
+            __syncwarp();
+            t.next(p, x);
+          }
+        }
+      }
     } else if (warp == 1) {
       // ---------------------------------------------------- MMA issue
       // The whole warp walks the tiles in step; one elected lane issues.  The
@@ -835,42 +886,6 @@ __global__ void __launch_bounds__(kStreamThreads, NT == 4 ? 1 : (D == 64 ? 3 : 2
   for (int key = done + threadIdx.x; key < end; key += kStreamThreads) p.score_out[base + key] = 0.f;
 }
 
-// -lse log2(e) in the order of the query tiles, two tiles per block.
-__global__ void __launch_bounds__(256) lse_kernel(const Params p) {
-  grid_dep_launch();
-  grid_dep_wait();
-  const long long tile = blockIdx.x * 2LL + (threadIdx.x >> 7);
-  const int c = threadIdx.x & 127;
-  if (tile >= static_cast<long long>(p.Bk) * p.Hkv * p.all) return;
-  const int bh = static_cast<int>(tile / p.all), f = static_cast<int>(tile - static_cast<long long>(bh) * p.all);
-  const int bk = bh / p.Hkv, hkv = bh - bk * p.Hkv;
-  float l = -INFINITY;
-  if (p.by_head) {
-    const int o = f / p.tiles, i = o / p.G, tok = 128 * (f - o * p.tiles) + c;
-    if (tok < p.T)
-      l = __ldg(p.lse + (static_cast<long long>(bk * p.n + i) * p.Hkv * p.G + hkv * p.G + o - i * p.G) * p.T + tok);
-  } else {
-    int i, r;
-    bool in;
-    if (p.GT >= 128) {
-      const int of = (p.GT + 127) / 128;
-      i = f / of;
-      r = 128 * (f - i * of) + c;
-      in = r < p.GT;
-    } else {
-      i = f * p.nb + c / p.GT;
-      r = c % p.GT;
-      in = c < p.nb * p.GT && i < p.n;
-    }
-    if (in) l = __ldg(p.lse + (static_cast<long long>(bk * p.n + i) * p.Hkv + hkv) * p.GT + r);
-  }
-  // a query that saw nothing (lse -inf) adds nothing
-  const bool none = l == -INFINITY;
-  p.nl[tile * kNl + c] = none ? -INFINITY : -l * kLog2e;
-  const bool any = __any_sync(0xffffffffu, none);  // (a warp is 32 columns of one tile)
-  if ((c & 31) == 0) p.nl[tile * kNl + 128 + (c >> 5)] = __int_as_float(any);
-}
-
 // score_out = score_in + the parts of a split unit, in order.
 __global__ void __launch_bounds__(256) weight_sum_kernel(const Params p) {
   grid_dep_launch();
@@ -947,9 +962,6 @@ cudaError_t run(const Params& p, const CUtensorMap& mq, const CUtensorMap& mk, i
   cudaError_t e = cudaFuncSetAttribute(weight_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  const long long tiles = static_cast<long long>(p.Bk) * p.Hkv * p.all;
-  e = launch_chained(lse_kernel, dim3(static_cast<unsigned>((tiles + 1) / 2)), dim3(256), 0, st, p);
-  if (e != cudaSuccess) return e;
   e = launch_chained(weight_kernel<D, FP16>, dim3(grid), dim3(kThreads), Cfg<D>::kSmem, st, mq, mk, p);
   if (e != cudaSuccess || p.Z == 1) return e;
   const long long n = static_cast<long long>(p.Bk) * p.Hkv * p.C;
@@ -957,7 +969,6 @@ cudaError_t run(const Params& p, const CUtensorMap& mq, const CUtensorMap& mk, i
 }
 
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
-size_t lse_bytes(const Params& p) { return static_cast<size_t>(p.Bk) * p.Hkv * p.all * kNl * 4; }
 
 bool streams(const Params& p, int d) {
   return static_cast<long long>(p.n) * p.GT <= (d == 64 ? kStreamRows<64> : kStreamRows<128>);
@@ -988,7 +999,7 @@ size_t weight_workspace_bytes(int B, int G, int Hkv, int T, int d, int Bk, int C
   Params p = {};
   if (!make_plan(p, B, G, Hkv, T, Bk, C)) return 0;
   if (streams(p, d)) return 256;
-  return 256 + align256(lse_bytes(p)) + align256(p.Z > 1 ? static_cast<size_t>(p.Z) * Bk * Hkv * C * 4 : 0);
+  return 256 + align256(p.Z > 1 ? static_cast<size_t>(p.Z) * Bk * Hkv * C * 4 : 0);
 }
 
 cudaError_t launch_weight(const WeightLaunch& a, cudaStream_t st) {
@@ -1001,8 +1012,7 @@ cudaError_t launch_weight(const WeightLaunch& a, cudaStream_t st) {
   p.causal = a.causal;
   p.scale_log2 = kLog2e / (a.d == 128 ? 11.313708498984761f : 8.0f);
   p.status = reinterpret_cast<int*>(a.ws);
-  p.nl = reinterpret_cast<float*>(a.ws + 256);
-  p.part = reinterpret_cast<float*>(a.ws + 256 + align256(lse_bytes(p)));
+  p.part = reinterpret_cast<float*>(a.ws + 256);
   if (streams(p, a.d)) {
     if (a.d == 128) return a.fp16 ? run_stream<128, true>(a, p, st) : run_stream<128, false>(a, p, st);
     return a.fp16 ? run_stream<64, true>(a, p, st) : run_stream<64, false>(a, p, st);
