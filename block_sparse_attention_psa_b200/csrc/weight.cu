@@ -53,7 +53,7 @@
 // 8 KV heads of 3, d = 64: 24 us, 5.1 TB/s (floor 19 us: the reads of K; of 64
 // caches of 4096 at d = 128 55 us, 5.9 TB/s). Last
 // 64 queries of a 128K prefill, 8 KV heads of 4, d = 128: 108 us (60:
-// exponentials). A whole 8K causal prefill of 32 heads: 351 us, 783 TFLOP/s
+// exponentials). A whole 8K causal prefill of 32 heads: 346 us, 795 TFLOP/s
 // (floors: 238 exponentials alone, 166 tensor core). A tile of 128 x 128 x 2
 // takes 2350 cycles, 1800 of them sums (88% of the exponential unit), the rest
 // hand-overs between tiles, and 2100 of 6100 between units of two tiles.
