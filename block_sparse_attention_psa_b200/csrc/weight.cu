@@ -40,9 +40,9 @@
 //    (64-token window 111 -> 107 us).
 //  * Units of equal cost (T < 128) lie on one line that is cut into equal
 //    runs; a prefill's go to the CTAs in turn, forwards and backwards, heaviest
-//    (fewest keys hidden) first.  When there are fewer units than two per SM the
-//    query tiles of a unit are split over several, whose sums a second kernel
-//    adds in a fixed order.
+//    (fewest keys hidden) first.  Where that leaves the last SM at work for longer
+//    the query tiles of a unit are split over several (make_plan), whose sums a
+//    second kernel adds in a fixed order.
 //  * One in eight exponentials runs on the FMA pipe (exp2_parts, 7.5e-8), whose
 //    other work leaves it half idle (8K prefill 354 -> 349 us, 64-token window
 //    121 -> 114; two in eight 348 and 117, three 380 and 127: the chains of
