@@ -4,7 +4,10 @@
 //
 // For one (sequence, KV head) with len entries and nk = min(len, budget):
 // every entry gets a 32-bit key that orders as its score does (protected
-// entries above all), the nk-th largest key K* is found by a radix select of
+// entries above all, with one key: which of them is first only matters where
+// more of them than nk, at positions that repeat or are negative, leave no room
+// for others; the cut then falls on that key, and the entries are keyed anew,
+// the protected ones by score), the nk-th largest key K* is found by a radix select of
 // 11 + 11 + 10 bits, and an entry stays iff key > K*, or key == K* and it is
 // among the first (nk - #{key > K*}) such entries in slot order.  Slots below
 // nk whose entry stays keep it; the r-th hole (ascending) takes the r-th
@@ -41,6 +44,8 @@ namespace cg = cooperative_groups;
 constexpr int kBins = 2048;
 constexpr int kSmemKeys = 32768;  // keys of a slice kept on chip (128 KB); a longer slice is read again per pass
 constexpr int kMaxThreads = 1024;
+constexpr uint32_t kSafe = 0xffffffffu;  // key of a protected entry (+inf has 0xff800000)
+constexpr uint32_t kBehind = 1u;         // of any other, where the protected ones rank by score (-inf has 0x007fffff)
 
 struct SelectParams {
   const float* score;
@@ -184,14 +189,16 @@ __global__ void __launch_bounds__(kMaxThreads, 1) select_kernel(const SelectPara
   // positions after `last - recent` are protected; 64 bits, so that no
   // position a caller stores can wrap it
   const long long guard = p.recent > 0 ? static_cast<long long>(last) - p.recent : LLONG_MAX;
+  bool scored = false;  // more entries are protected than stay: they rank by score
   auto make_key = [&](int i) -> uint32_t {
     const int at = pos ? __ldg(pos + i) : i;
     const uint32_t k = score_key(__ldg(score + i));
-    return at < p.sink || at > guard ? 0xffffffffu : k;
+    const bool safe = at < p.sink || at > guard;
+    return scored ? (safe ? k : kBehind) : (safe ? kSafe : k);
   };
   if (guarded && p.pos_on_chip) {
     for (int i = tid; i < s1 - s0; i += nthr)
-      if (spos[i] < p.sink || spos[i] > guard) keys[i] = 0xffffffffu;
+      if (spos[i] < p.sink || spos[i] > guard) keys[i] = kSafe;
   } else if (p.keys_on_chip) {
 #pragma unroll 8
     for (int i = s0 + tid; i < s1; i += nthr) keys[i - s0] = make_key(i);
@@ -200,19 +207,19 @@ __global__ void __launch_bounds__(kMaxThreads, 1) select_kernel(const SelectPara
   if (p.keys_on_chip)
     for (int i = max(s1 - s0, 0) + tid; i < p.slice; i += nthr) keys[i] = 0u;
   auto key = [&](int i) -> uint32_t { return p.keys_on_chip ? keys[i - s0] : (i < s1 ? make_key(i) : 0u); };
+  auto score_safe = [&]() {
+    scored = true;
+    if (p.keys_on_chip)
+      for (int i = tid; i < s1 - s0; i += nthr)
+        keys[i] = keys[i] == kSafe ? score_key(__ldg(score + s0 + i)) : kBehind;
+  };
   __syncthreads();
 
   if (len - nk == 1) {
     // ---- one entry goes (a decode step at its budget): the lowest key, of
     // equal ones the last; slot nk takes its place.  One reduction instead of
     // three rounds and the ranks: a call on 1025 entries 11.7 -> 5.6 us.
-    uint32_t hi = 0xffffffffu, lo = 0xffffffffu;  // key, ~slot
-#pragma unroll 4
-    for (int i = s0 + tid; i < s1; i += nthr) {
-      const uint32_t k = key(i);
-      if (k <= hi) hi = k, lo = ~static_cast<uint32_t>(i);
-    }
-    __syncwarp();
+    uint32_t hi, lo;  // key, ~slot
     auto lowest = [&]() {
       const uint32_t k = __reduce_min_sync(0xffffffffu, hi);
       lo = __reduce_min_sync(0xffffffffu, hi == k ? lo : 0xffffffffu);
@@ -222,18 +229,31 @@ __global__ void __launch_bounds__(kMaxThreads, 1) select_kernel(const SelectPara
       hi = there ? static_cast<uint32_t>(v.x) : 0xffffffffu;
       lo = there ? static_cast<uint32_t>(v.y) : 0xffffffffu;
     };
-    lowest();
-    if (lane == 0) buf[warp] = make_int2(static_cast<int>(hi), static_cast<int>(lo));
-    __syncthreads();
-    __syncwarp();
-    give(lane < (nthr >> 5) ? buf[lane] : make_int2(0, 0), lane < (nthr >> 5));
-    lowest();
-    if constexpr (CL) {
-      if (tid == 0) sh.count[0] = make_int2(static_cast<int>(hi), static_cast<int>(lo));
-      cl.sync();
+#pragma unroll 1
+    for (;;) {
+      hi = lo = 0xffffffffu;
+#pragma unroll 4
+      for (int i = s0 + tid; i < s1; i += nthr) {
+        const uint32_t k = key(i);
+        if (k <= hi) hi = k, lo = ~static_cast<uint32_t>(i);
+      }
       __syncwarp();
-      give(lane < ncta ? peer(lane)->count[0] : make_int2(0, 0), lane < ncta);
       lowest();
+      if (lane == 0) buf[warp] = make_int2(static_cast<int>(hi), static_cast<int>(lo));
+      __syncthreads();
+      __syncwarp();
+      give(lane < (nthr >> 5) ? buf[lane] : make_int2(0, 0), lane < (nthr >> 5));
+      lowest();
+      if constexpr (CL) {
+        if (tid == 0) sh.count[scored] = make_int2(static_cast<int>(hi), static_cast<int>(lo));
+        cl.sync();
+        __syncwarp();
+        give(lane < ncta ? peer(lane)->count[scored] : make_int2(0, 0), lane < ncta);
+        lowest();
+      }
+      if (uniform(scored || hi != kSafe)) break;
+      score_safe();     // every entry is protected
+      __syncthreads();  // `buf` has been read
     }
     const int gone = static_cast<int>(~lo);
     for (int i = s0 + tid; i < min(s1, nk); i += nthr) kept[i] = i == gone ? nk : i;
@@ -338,6 +358,14 @@ __global__ void __launch_bounds__(kMaxThreads, 1) select_kernel(const SelectPara
     need -= static_cast<uint32_t>(uniform(pick[1]));
     equal = static_cast<uint32_t>(uniform(pick[2]));
     // (the next round's barriers keep `pick` until all have read)
+    if (round == 0 && !scored && prefix == kSafe >> 21 && need < equal) {
+      // more protected entries than nk: once more, with the keys of that case
+      sync_all();  // all have read the histograms
+      score_safe();
+      for (int i = tid; i < kBins; i += nthr) sh.hist[0][i] = 0u;
+      prefix = 0, need = static_cast<uint32_t>(nk), equal = 0, round = -1;
+      __syncthreads();
+    }
   }
   // prefix is K* (its bits from `shift` on); of the `equal` entries with them
   // the first `need` stay

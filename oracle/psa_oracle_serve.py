@@ -95,7 +95,7 @@ def evict(score, pos, cache_len, budget, sink, recent):
             def rank(i):
                 s = float(score[b, h, i])
                 safe = ps[i] < sink or int(ps[i]) > last - recent
-                return (0 if safe else 1, 0.0 if safe else (math.inf if math.isnan(s) else -s), i)
+                return (0 if safe else 1, math.inf if math.isnan(s) else -s, i)
 
             stay = sorted(sorted(range(m), key=rank)[:nk])
             inside = set(i for i in stay if i < nk)
