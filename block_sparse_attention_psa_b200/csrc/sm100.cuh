@@ -131,6 +131,20 @@ __device__ __forceinline__ void named_barrier_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// The same, telling all of them whether any came with `p`.
+__device__ __forceinline__ bool named_barrier_or(int id, int nthreads, bool p) {
+  int any;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\t"
+      "setp.ne.b32 a, %3, 0;\n\t"
+      "bar.red.or.pred b, %1, %2, a;\n\t"
+      "selp.b32 %0, 1, 0, b;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(nthreads), "r"(static_cast<int>(p))
+      : "memory");
+  return any != 0;
+}
+
 // ---------------------------------------------------------------- launch chaining
 // Programmatic dependent launch.  A kernel of this library launched with the
 // programmatic-serialization attribute may start while the kernel before it

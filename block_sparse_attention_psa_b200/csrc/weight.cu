@@ -610,6 +610,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     int nu = 0, qt = 0, it = 0, joins = 0;
     bool ok = true, met = false;
     const int pair_bar = 1 + 4 * s + (warp & 3);  // named barrier of the two warps of a row
+    // The two warps of a row meet once per pair of key tiles, and once more when
+    // they leave.  Each says there whether it has given up or seen that another
+    // did, and the barrier gives both the same answer: they part at one meeting,
+    // and none waits there for a partner that is gone.  (The abort flag itself
+    // may change between two looks at it.)
+    auto meet = [&](bool gone) -> bool { return named_barrier_or(pair_bar, 64, gone || *abort_flag); };
     for (;;) {
       const int slot = nu % kRing;
       ok = mbar_sleep_warp(&u_full[slot], (nu / kRing) & 1, abort_flag, p.status);
@@ -715,11 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++joins;
         if (half) hs[row] = acc;
         __syncwarp();
-        named_barrier_sync(pair_bar, 64);
-        if (*abort_flag) {
-          met = true;  // the barrier was this warp's last
-          break;
-        }
+        if ((met = meet(false))) break;
         if (!half) acc += hs[row];
         if (!half && key < p.C) {
           if (p.Z > 1) {
@@ -731,9 +733,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok || met) break;
     }
-    // After a timeout the two warps of a row meet once more: one that gave up
-    // here, or at the barrier of its unit, where it then sees the flag.
-    if (!ok && !met) named_barrier_sync(pair_bar, 64);
+    __syncwarp();
+    if (!met) meet(true);
     // units of a line end at the keys: the slots of the pairs behind them
     if (!p.by_head && p.Z == 1) {
       const int tid = threadIdx.x - 128;
