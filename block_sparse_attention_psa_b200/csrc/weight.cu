@@ -491,8 +491,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         Unit x;
         next_unit(x, false);
         __syncwarp();
+        // (lanes wait for themselves: one whose wait ran out has no unit)
+        if (!__all_sync(0xffffffffu, x.nt >= 0)) break;
         const int nt = uniform(x.nt), np = uniform(x.np);
-        if (nt < 0) break;
         if (lane == 0) mbar_arrive(&u_empty[(nu - 1) % kRing]);
         __syncwarp();
         for (int pp = 0; ok && pp < (p.resident ? 1 : np); ++pp) {
@@ -547,8 +548,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         Unit x;
         next_unit(x, false);
         __syncwarp();
+        // (lanes wait for themselves: one whose wait ran out has no unit)
+        if (!__all_sync(0xffffffffu, x.nt >= 0)) break;
         const int nt = uniform(x.nt), np = uniform(x.np);
-        if (nt < 0) break;
         if (elect_one()) mbar_arrive(&u_empty[(nu - 1) % kRing]);
         __syncwarp();
         if (nt == 0) continue;

@@ -50,3 +50,13 @@ def test_the_rule_in_all_combinations():
                 answer = any(last[w] or j >= sees[w] for w in (0, 1))
                 left = [answer or x for x in last]
             assert left == [True, True]
+
+
+def test_a_warp_uses_a_unit_only_if_every_lane_has_it():
+    """Lanes of the lse and the MMA warp wait for the next unit one by one; after
+    a timeout one may come back without a unit while lane 0 has one, and its
+    fields are then not to be used (the lse warp makes addresses of them)."""
+    parts = _code().split("next_unit(x, false);")
+    assert len(parts) == 3
+    for after in parts[1:]:
+        assert re.match(r"\s*__syncwarp\(\);\s*if \(!__all_sync\(0xffffffffu, x\.nt >= 0\)\) break;", after)
