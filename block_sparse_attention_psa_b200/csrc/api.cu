@@ -606,7 +606,7 @@ int psa_decode(const void* q, const void* k_prefix, const void* v_prefix, const 
     for (int j = 0; j < i; ++j)
       if (overlap(outs[i], outs[j])) return PSA_ERR_ARG;
   }
-  if ((s = check_device({q, k_prefix, k_cache, out, workspace})) !=
+  if ((s = check_device({q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, cache_len, out, lse, workspace})) !=
       PSA_OK)
     return s;
   psa::DecodeLaunch a = {};
@@ -656,7 +656,7 @@ int psa_key_weight(const void* q, const void* k, const float* lse, const int* ke
       (key_len && overlap(out, {key_len, static_cast<size_t>(Bk) * 4})) || overlap(out, {workspace, need}) ||
       (score_in != score_out && overlap(out, {score_in, slots * 4})))
     return PSA_ERR_ARG;
-  if ((s = check_device({q, k, score_out, workspace})) != PSA_OK) return s;
+  if ((s = check_device({q, k, lse, key_len, score_in, score_out, workspace})) != PSA_OK) return s;
   psa::WeightLaunch a = {};
   a.q = q;
   a.k = k;
@@ -718,7 +718,8 @@ int psa_cache_evict(const void* k, const void* v, const float* score, const int*
     for (int j = 0; j < i; ++j)
       if (overlap(outs[i], outs[j])) return PSA_ERR_ARG;
   }
-  if ((s = check_device({k, score, k_out, workspace})) != PSA_OK)
+  if ((s = check_device({k, v, score, pos, cache_len, k_out, v_out, score_out, pos_out, len_out, kept, workspace})) !=
+      PSA_OK)
     return s;
   char* ws = static_cast<char*>(workspace);
   psa::EvictLaunch a = {};
