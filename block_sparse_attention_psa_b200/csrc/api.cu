@@ -651,11 +651,12 @@ int psa_key_weight(const void* q, const void* k, const float* lse, const int* ke
   const size_t need = psa::weight_workspace_bytes(B, Hq / Hkv, Hkv, T, d, Bk, C);
   if (workspace_bytes < need) return PSA_ERR_CAPACITY;
   const size_t rows = static_cast<size_t>(B) * Hq * T, slots = static_cast<size_t>(Bk) * Hkv * C;
-  const Range out = {score_out, slots * 4};
-  if (overlap(out, {q, rows * d * 2}) || overlap(out, {k, slots * d * 2}) || overlap(out, {lse, rows * 4}) ||
-      (key_len && overlap(out, {key_len, static_cast<size_t>(Bk) * 4})) || overlap(out, {workspace, need}) ||
-      (score_in != score_out && overlap(out, {score_in, slots * 4})))
-    return PSA_ERR_ARG;
+  const Range ins[] = {{q, rows * d * 2}, {k, slots * d * 2}, {lse, rows * 4}, {key_len, static_cast<size_t>(Bk) * 4},
+                       {score_in, slots * 4}};
+  const Range out = {score_out, slots * 4}, work = {workspace, need};
+  for (int i = 0; i < 5; ++i)  // (the scores themselves may be added to in place)
+    if ((!(i == 4 && score_in == score_out) && overlap(out, ins[i])) || overlap(work, ins[i])) return PSA_ERR_ARG;
+  if (overlap(out, work)) return PSA_ERR_ARG;
   if ((s = check_device({q, k, lse, key_len, score_in, score_out, workspace})) != PSA_OK) return s;
   psa::WeightLaunch a = {};
   a.q = q;

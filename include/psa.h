@@ -366,7 +366,7 @@ PSA_API int psa_decode(const void* q, const void* k_prefix, const void* v_prefix
  *   tokens themselves: T = key_len is a causal prefill, a small T an
  *   observation window or a decode step).
  * score_in may be NULL (zero) or score_out itself (accumulate in place); any
- * other overlap of score_out is refused.  T, C <= 2^20.  Sums are float32,
+ * other overlap of score_out, or of the workspace, is refused.  T, C <= 2^20.  Sums are float32,
  * in a fixed order.
  * Errors: PSA_ERR_ARG, PSA_ERR_SHAPE, PSA_ERR_UNSUPPORTED, PSA_ERR_CAPACITY,
  * PSA_ERR_DEVICE, PSA_ERR_CUDA.
