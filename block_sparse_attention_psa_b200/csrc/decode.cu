@@ -112,8 +112,8 @@ struct Piece {
 constexpr int kPieceInts = sizeof(Piece) / 4;
 
 __device__ __forceinline__ int seg_len(const Params& p, int s) {
-  if (s < p.npre) return min(max(p.prefix_len ? __ldg(p.prefix_len + s) : p.P, 0), p.P);
-  return min(max(p.cache_len ? __ldg(p.cache_len + s - p.npre) : p.C, 0), p.C);
+  if (s < p.npre) return min(max(p.prefix_len ? p.prefix_len[s] : p.P, 0), p.P);
+  return min(max(p.cache_len ? p.cache_len[s - p.npre] : p.C, 0), p.C);
 }
 __device__ __forceinline__ bool seg_bad(const Params& p, int s) {
   if (s < p.npre) return p.prefix_len && (p.prefix_len[s] < 0 || p.prefix_len[s] > p.P);

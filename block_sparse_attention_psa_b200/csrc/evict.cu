@@ -128,14 +128,14 @@ __global__ void __launch_bounds__(kMaxThreads, 1) select_kernel(const SelectPara
   grid_dep_launch();
   grid_dep_wait();
 
-  int len = p.cache_len ? __ldg(p.cache_len + b) : p.C;
+  int len = p.cache_len ? p.cache_len[b] : p.C;
   len = uniform(min(max(len, 0), p.C));
   if (blockIdx.x == 0) {
     // one writer of the status word: the lengths of all sequences
     bool bad = false;
     if (p.cache_len)
       for (int i = tid; i < p.B; i += nthr) {
-        const int n = __ldg(p.cache_len + i);
+        const int n = p.cache_len[i];
         bad |= n < 0 || n > p.C;
       }
     bad = __syncthreads_or(bad);
@@ -163,15 +163,15 @@ __global__ void __launch_bounds__(kMaxThreads, 1) select_kernel(const SelectPara
     if (p.pos_on_chip) {
 #pragma unroll 8
       for (int i = s0 + tid; i < s1; i += nthr) {
-        const int at = __ldg(pos + i);
-        const float f = __ldg(score + i);
+        const int at = pos[i];
+        const float f = score[i];
         spos[i - s0] = at;
         keys[i - s0] = score_key(f);
         last = max(last, at);
       }
     } else {
 #pragma unroll 8
-      for (int i = s0 + tid; i < s1; i += nthr) last = max(last, __ldg(pos + i));
+      for (int i = s0 + tid; i < s1; i += nthr) last = max(last, pos[i]);
     }
     __syncwarp();
     last = __reduce_max_sync(0xffffffffu, last);
@@ -191,8 +191,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) select_kernel(const SelectPara
   const long long guard = p.recent > 0 ? static_cast<long long>(last) - p.recent : LLONG_MAX;
   bool scored = false;  // more entries are protected than stay: they rank by score
   auto make_key = [&](int i) -> uint32_t {
-    const int at = pos ? __ldg(pos + i) : i;
-    const uint32_t k = score_key(__ldg(score + i));
+    const int at = pos ? pos[i] : i;
+    const uint32_t k = score_key(score[i]);
     const bool safe = at < p.sink || at > guard;
     return scored ? (safe ? k : kBehind) : (safe ? kSafe : k);
   };
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) select_kernel(const SelectPara
     scored = true;
     if (p.keys_on_chip)
       for (int i = tid; i < s1 - s0; i += nthr)
-        keys[i] = keys[i] == kSafe ? score_key(__ldg(score + s0 + i)) : kBehind;
+        keys[i] = keys[i] == kSafe ? score_key(score[s0 + i]) : kBehind;
   };
   __syncthreads();
 
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) 
 #pragma unroll
   for (int j = 0; j < kSteps; ++j) {
     const int i = slot0 + warp * kPerWarp + j * kRows + sub;
-    src[j] = i < p.budget ? __ldg(kept + i) : -1;
+    src[j] = i < p.budget ? kept[i] : -1;
     if (p.in_place && src[j] == i) src[j] = -1;
   }
 #pragma unroll
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) 
     }
   if (threadIdx.x < kMoveSlots) {
     const int i = slot0 + threadIdx.x;
-    const int s = i < p.budget ? __ldg(kept + i) : -1;
+    const int s = i < p.budget ? kept[i] : -1;
     if (s >= 0) {
       // in place a slot that stays still needs its position when none came in
       if (!(p.in_place && s == i)) p.score_out[out0 + i] = p.score[in0 + s];
