@@ -846,9 +846,11 @@ __global__ void __launch_bounds__(kStreamThreads, NT == 4 ? 1 : (D == 64 ? 3 : 2
       const int i2 = r2 / p.GT, rr2 = r2 - i2 * p.GT;
       float l = -INFINITY;
       if (r2 < rows) l = p.lse[(static_cast<long long>(bk * p.n + i2) * p.Hkv + hkv) * p.GT + rr2];
-      // a query that saw nothing (lse -inf) adds nothing
-      nl[j][e] = l == -INFINITY ? -INFINITY : -l * kLog2e;
-      lim[j][e] = r2 >= rows ? -1 : (p.causal ? len - p.T + rr2 % p.T : INT_MAX);
+      // a query that saw nothing (lse -inf) adds nothing, to keys of NaN or
+      // infinities neither (0 of the query times such a key is NaN)
+      const bool none = l == -INFINITY;
+      nl[j][e] = none ? -INFINITY : -l * kLog2e;
+      lim[j][e] = none ? -1 : (p.causal ? len - p.T + rr2 % p.T : INT_MAX);
     }
   }
   for (; key0 < min(end, len); key0 += 16 * kWarps) {
