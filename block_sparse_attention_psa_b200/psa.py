@@ -22,11 +22,6 @@ import os
 
 import torch
 
-try:
-    from . import _call as _native
-except ImportError:   # not built for this PyTorch: the same calls, some 10 us slower on the host
-    _native = None
-
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpsa.so")
 
@@ -93,15 +88,32 @@ def _declare(L: ctypes.CDLL) -> None:
         fn.argtypes = args
 
 
+def _load_native():
+    """The module ``_call``, or None: the same calls, some 10 us slower on the host."""
+    try:
+        from . import _call
+    except ImportError:
+        return None
+    return _call
+
+
+def __getattr__(name):
+    if name == "_native":   # loaded with the library, not on import
+        lib()
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
 def lib() -> ctypes.CDLL:
-    """The loaded library (raises if it has not been built)."""
-    global _lib
+    """The loaded library (raises if it has not been built), and with it ``_call.so``."""
+    global _lib, _native
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is missing; build it with "
                                "`python -m block_sparse_attention_psa_b200.build`")
         L = ctypes.CDLL(LIB_PATH)
         _declare(L)
+        _native = _load_native()
         if _native is not None:
             _native.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
                 L.psa_decode, L.psa_decode_workspace_size, L.psa_key_weight, L.psa_key_weight_workspace_size,
@@ -506,6 +518,8 @@ def psa_decode(q, k_cache=None, v_cache=None, cache_len=None, k_prefix=None, v_p
     if stream is not None:   # what is allocated here then belongs to that stream
         with torch.cuda.stream(stream):
             return psa_decode(q, k_cache, v_cache, cache_len, k_prefix, v_prefix, prefix_len, ws, out, lse, want_lse)
+    if _lib is None:
+        lib()
     if _native is not None:
         r = _native.decode(q, k_cache, v_cache, cache_len, k_prefix, v_prefix, prefix_len, ws, out, lse, want_lse)
         if r is not None:
@@ -568,6 +582,8 @@ def psa_key_weight(q, k, lse, key_len=None, causal: bool = False, score=None, ws
     if stream is not None:
         with torch.cuda.stream(stream):
             return psa_key_weight(q, k, lse, key_len, causal, score, ws, out)
+    if _lib is None:
+        lib()
     if _native is not None:
         r = _native.key_weight(q, k, lse, key_len, causal, score, ws, out)
         if r is not None:
@@ -614,6 +630,8 @@ def psa_cache_evict(k, v, score, budget: int, pos=None, cache_len=None, sink: in
     if stream is not None:
         with torch.cuda.stream(stream):
             return psa_cache_evict(k, v, score, budget, pos, cache_len, sink, recent, ws, out)
+    if _lib is None:
+        lib()
     if _native is not None:
         r = _native.cache_evict(k, v, score, budget, pos, cache_len, sink, recent, ws, out)
         if r is not None:
