@@ -23,6 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpsa.so")
 CALL = os.path.join(PKG, "_call.so")
+CALL_STAMP = os.path.join(BUILD, "call.built_for")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -55,29 +56,45 @@ def _compile(src: str, ptxas_v: bool) -> tuple[str, str]:
     return obj, r.stderr
 
 
+def built_for() -> str:
+    """The PyTorch and Python of this process, whose layouts ``_call.so`` has compiled in."""
+    import torch
+
+    return f"torch {torch.__version__} {torch.version.git_version} {sys.implementation.cache_tag}"
+
+
+def _call_is_current(sources) -> bool:
+    try:
+        with open(CALL_STAMP) as f:
+            return f.read() == built_for() and os.path.getmtime(CALL) >= max(os.path.getmtime(p) for p in sources)
+    except OSError:
+        return False
+
+
 def _build_call() -> str:
-    """The native form of the binding's serving calls, against the PyTorch it
-    is used with (a newer PyTorch builds it anew)."""
+    """The native form of the binding's serving calls, against the PyTorch and
+    Python it is used with (others build it anew)."""
     import sysconfig
 
     import torch
     from torch.utils import cpp_extension as ext
 
     src = os.path.join(CSRC, "call.cpp")
-    newest = max(os.path.getmtime(p) for p in (src, os.path.join(INCLUDE, "psa.h"), torch.__file__))
-    if os.path.exists(CALL) and os.path.getmtime(CALL) >= newest:
+    if _call_is_current((src, os.path.join(INCLUDE, "psa.h"), torch.__file__)):
         return CALL
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     inc = [INCLUDE, *ext.include_paths(), os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = f"{CALL}.{os.getpid()}"   # a process that has the old one mapped keeps it
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *(f"-isystem{p}" for p in inc), src,
-           "-o", tmp, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f'-DPSA_BUILT_FOR="{built_for()}"',
+           *(f"-isystem{p}" for p in inc), src, "-o", tmp, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALL)
+    with open(CALL_STAMP, "w") as f:
+        f.write(built_for())
     return CALL
 
 

@@ -348,4 +348,10 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_call", nullptr, -1, methods, null
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__call() { return PyModule_Create(&module); }
+// built_for: the PyTorch and Python whose layouts are compiled in (psa.py uses
+// the module with no other)
+PyMODINIT_FUNC PyInit__call() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", PSA_BUILT_FOR) < 0) Py_CLEAR(m);
+  return m;
+}

@@ -22,6 +22,8 @@ import os
 
 import torch
 
+from . import build
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpsa.so")
 
@@ -89,12 +91,14 @@ def _declare(L: ctypes.CDLL) -> None:
 
 
 def _load_native():
-    """The module ``_call``, or None: the same calls, some 10 us slower on the host."""
+    """The module ``_call`` if it is there and built for this PyTorch and Python
+    (it reads tensors by their layout), else None: the same calls, some 10 us
+    slower on the host."""
     try:
         from . import _call
     except ImportError:
         return None
-    return _call
+    return _call if getattr(_call, "built_for", None) == build.built_for() else None
 
 
 def __getattr__(name):

@@ -4,6 +4,8 @@ import os
 import subprocess
 import sys
 
+from block_sparse_attention_psa_b200 import build, psa
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
@@ -41,3 +43,30 @@ for call in (lambda: psa.psa_decode(q, k, k), lambda: psa.psa_key_weight(q, k, t
 print(psa._native.__name__)
 """)
     assert out.split("\n") == 3 * ["tensor must live on a CUDA device"] + ["block_sparse_attention_psa_b200._call", ""]
+
+
+def test_it_serves_only_the_pytorch_it_was_built_for(monkeypatch):
+    assert psa._native is not None and psa._native.built_for == build.built_for()
+    monkeypatch.setattr(build, "built_for", lambda: "torch 9.9.9 cpython-399")
+    assert psa._load_native() is None
+
+
+def test_another_pytorch_builds_it_anew(monkeypatch, tmp_path):
+    """Whatever the files' times say."""
+    made = []
+
+    def compiler(cmd, **kw):
+        made.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(build, "CALL", str(tmp_path / "_call.so"))
+    monkeypatch.setattr(build, "CALL_STAMP", str(tmp_path / "stamp"))
+    monkeypatch.setattr(build.subprocess, "run", compiler)
+    build._build_call()
+    build._build_call()
+    assert len(made) == 1
+    monkeypatch.setattr(build, "built_for", lambda: "torch 9.9.9 cpython-399")
+    build._build_call()
+    build._build_call()
+    assert len(made) == 2 and any("torch 9.9.9 cpython-399" in x for x in made[1])
