@@ -100,13 +100,20 @@ def _build_call() -> str:
 
 def build(ptxas_v: bool = False, verbose: bool = False) -> str:
     """Compile every CUDA source for sm_100a and link ``libpsa.so``, and the
-    binding's ``_call.so``."""
+    binding's ``_call.so``.  The library needs nvcc alone; where ``_call.so``
+    cannot be built (no PyTorch, no Python headers, no g++) the binding does
+    without it, and this says why on stderr."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
         call = ex.submit(_build_call)
         results = list(ex.map(lambda s: _compile(s, ptxas_v), srcs))
-        call.result()
+        try:
+            call.result()
+        except Exception as e:
+            if os.path.exists(CALL):   # of other sources: its calls may not be the library's
+                os.remove(CALL)
+            sys.stderr.write(f"_call.so is not built (the serving calls take longer on the host): {e}\n")
     objs = [o for o, _ in results]
     if verbose or ptxas_v:
         for _, log in results:
