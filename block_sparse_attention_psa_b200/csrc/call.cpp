@@ -206,7 +206,7 @@ PyObject* weight_call(PyObject* const* a) {
   const void* k = x.at(a[1], keys, q->scalar_type());
   const float* lse = x.at<float>(a[2], rows, at::kFloat);
   const int* len = x.at<int>(a[3], nk, at::kInt);
-  const int causal = PyObject_IsTrue(a[4]);
+  const int causal = a[4] == Py_True ? 1 : (a[4] == Py_False ? 0 : -1);  // (psa.py says what else counts as one)
   const float* score = x.at<float>(a[5], slots, at::kFloat);
   float* out = x.at<float>(a[7], slots, at::kFloat);
   at::Tensor ws_own, out_own;
