@@ -468,6 +468,15 @@ def _arg(name, t, like, shape, dtype):
     return t.data_ptr()
 
 
+def _on_stream(stream, like):
+    """The given stream as the current one: what is allocated under it then
+    belongs to it.  It has to be of the problem's device, whose current stream
+    the call takes."""
+    if stream.device != like.device:
+        raise ValueError(f"stream is on {stream.device}, the problem on {like.device}")
+    return torch.cuda.stream(stream)
+
+
 def _serve(fn, like, *args):
     """Call a serving entry point on the problem's device and its current
     stream."""
@@ -519,8 +528,8 @@ def psa_decode(q, k_cache=None, v_cache=None, cache_len=None, k_prefix=None, v_p
     last T valid cache entries are the new tokens (query t sees slots below
     cache_len - (T - 1 - t)).  Returns out and, if requested, lse (float32
     [B, Hq, T])."""
-    if stream is not None:   # what is allocated here then belongs to that stream
-        with torch.cuda.stream(stream):
+    if stream is not None:
+        with _on_stream(stream, q):
             return psa_decode(q, k_cache, v_cache, cache_len, k_prefix, v_prefix, prefix_len, ws, out, lse, want_lse)
     if _lib is None:
         lib()
@@ -584,7 +593,7 @@ def psa_key_weight(q, k, lse, key_len=None, causal: bool = False, score=None, ws
     below key_len - (T - 1 - t)).  Slots past ``key_len`` get 0.  ``out`` may
     be ``score`` itself."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, q):
             return psa_key_weight(q, k, lse, key_len, causal, score, ws, out)
     if _lib is None:
         lib()
@@ -632,7 +641,7 @@ def psa_cache_evict(k, v, score, budget: int, pos=None, cache_len=None, sink: in
     length).  ``out`` gives these six buffers instead; with the inputs
     themselves as the first four the eviction is in place."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, k):
             return psa_cache_evict(k, v, score, budget, pos, cache_len, sink, recent, ws, out)
     if _lib is None:
         lib()
