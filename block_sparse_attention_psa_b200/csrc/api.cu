@@ -133,6 +133,10 @@ std::atomic<int> g_stall_request{0};
 
 int take_stall_request() { return g_stall_request.exchange(0); }
 
+std::atomic<int> g_serve_stall_request{0};
+
+int take_serve_stall_request() { return g_serve_stall_request.exchange(0); }
+
 }  // namespace psa
 
 using psa::kBlock;
@@ -556,6 +560,12 @@ int psa_dense(const psa_bf16_t* q, const psa_bf16_t* k, const psa_bf16_t* v, int
 int psa_test_stall_next_attn(int on) {
   if (on != 0 && on != 1) return PSA_ERR_ARG;
   psa::g_stall_request.store(on);
+  return PSA_OK;
+}
+
+int psa_test_stall_next_serve(int on) {
+  if (on != 0 && on != 1) return PSA_ERR_ARG;
+  psa::g_serve_stall_request.store(on);
   return PSA_OK;
 }
 

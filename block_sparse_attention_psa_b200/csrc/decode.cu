@@ -96,6 +96,7 @@ struct Params {
   float* part_o;       // parts: rows x d
   float2* part_ml;     // reference (log2 units), sum
   int* status;
+  int stall;           // test hook: CTA 0 withholds its first S hand-off
 };
 
 // A piece: part of one unit's key tiles, as the scheduler publishes it.
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int kk = 0; kk < D / 16; ++kk)
               tc_mma_bf16(ds, a + (kk >> 2) * 1024 + (kk & 3) * 2, b + (kk >> 2) * 1024 + (kk & 3) * 2, kIdescS,
                           kk ? 1u : 0u);
-            tc_commit(&s_full[s]);
+            if (!(p.stall && blockIdx.x == 0 && cnt == 0)) tc_commit(&s_full[s]);
             if (tile_end) tc_commit(&k_empty[st]);
             if (i >= ni - 1 - pair) tc_commit(&q_empty[qs]);
           }
@@ -1051,6 +1052,7 @@ cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t st) {
   p.unit_ctas = reinterpret_cast<int2*>(a.ws + w.off_units);
   p.part_ml = reinterpret_cast<float2*>(a.ws + w.off_ml);
   p.part_o = reinterpret_cast<float*>(a.ws + w.off_o);
+  p.stall = take_serve_stall_request();
   // Q: [B][Hkv][G T][d]; prefix tiles take pre_nb sequences at once
   CUtensorMap m[6];
   const uint64_t u = 1;

@@ -222,6 +222,8 @@ cudaError_t launch_evict(const EvictLaunch& a, cudaStream_t st);
 
 // api.cu: one-shot flag set by psa_test_stall_next_attn, taken by the next psa_attn
 int take_stall_request();
+// the same of psa_test_stall_next_serve, taken by the next tensor-core kernel of decode.cu or weight.cu
+int take_serve_stall_request();
 
 // api.cu: driver entry point for cuTensorMapEncodeTiled (resolved once)
 CUresult encode_tensor_map_3d_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows,

@@ -107,6 +107,7 @@ struct Params {
   long long units;
   float scale_log2;
   int* status;
+  int stall;              // test hook: CTA 0 withholds its first hand-off of S^T
 };
 
 // A unit, as the scheduler publishes it.
@@ -574,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int kk = 0; kk < D / 16; ++kk)
                 tc_mma_bf16(tbase + 128 * buf, a + (kk >> 2) * 1024 + (kk & 3) * 2,
                             b + (kk >> 2) * 1024 + (kk & 3) * 2, idesc, kk ? 1u : 0u);
-              tc_commit(&s_full[buf]);
+              if (!(p.stall && blockIdx.x == 0 && it == 0)) tc_commit(&s_full[buf]);
             }
             if (!r1) ok &= mbar_sleep(&s_empty[2 + buf], eh, abort_flag, p.status);
             __syncwarp();
@@ -1024,6 +1025,7 @@ cudaError_t launch_weight(const WeightLaunch& a, cudaStream_t st) {
     if (a.d == 128) return a.fp16 ? run_stream<128, true>(a, p, st) : run_stream<128, false>(a, p, st);
     return a.fp16 ? run_stream<64, true>(a, p, st) : run_stream<64, false>(a, p, st);
   }
+  p.stall = take_serve_stall_request();
   p.resident = !p.by_head && p.Z == 1 && p.all <= (a.d == 128 ? Cfg<128>::kQStages : Cfg<64>::kQStages);
   CUtensorMap mq, mk;
   const uint64_t u = 1;

@@ -46,7 +46,7 @@ EXPORTS = ("psa_status_string", "psa_version", "psa_workspace_size", "psa_route_
            "psa_attn_noalloc", "psa_route_thresh_prob", "psa_test_stall_next_attn",
            "psa_read_fixup_count", "psa_hyd_stat", "psa_attn_hyd", "psa_attn_bwd", "psa_decode_workspace_size",
            "psa_decode", "psa_key_weight_workspace_size", "psa_key_weight", "psa_cache_evict_workspace_size",
-           "psa_cache_evict")
+           "psa_cache_evict", "psa_test_stall_next_serve")
 
 _lib = None
 
@@ -82,6 +82,7 @@ def _declare(L: ctypes.CDLL) -> None:
         "psa_cache_evict_workspace_size": (Z, [I] * 4),
         "psa_cache_evict": (I, [P] * 5 + [I] * 8 + [P] * 7 + [Z, P]),
         "psa_test_stall_next_attn": (I, [I]),
+        "psa_test_stall_next_serve": (I, [I]),
         "psa_attn_noalloc": (I, [P, P, P, P, P, P, P, Z, P, I, I, I, I, I, I, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
@@ -685,6 +686,11 @@ def psa_test_stall_next_attn(on: bool = True) -> None:
     """Failure-path test hook: the next psa_attn call's kernel lets a bounded
     wait run out and records PSA_ERR_TIMEOUT in its workspace status word."""
     _check("psa_test_stall_next_attn", lib().psa_test_stall_next_attn(int(bool(on))))
+
+
+def psa_test_stall_next_serve(on: bool = True) -> None:
+    """The same for the next psa_decode, or psa_key_weight of many queries."""
+    _check("psa_test_stall_next_serve", lib().psa_test_stall_next_serve(int(bool(on))))
 
 
 def psa_read_status(ws, stream=None) -> int:

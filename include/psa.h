@@ -415,6 +415,14 @@ PSA_API int psa_cache_evict(const void* k, const void* v, const float* score, co
 PSA_API int psa_test_stall_next_attn(int on);
 
 /*
+ * The same for the serving operators: the next psa_decode, or psa_key_weight
+ * of more queries per key than its streaming kernel takes (32 at d = 64, 16 at
+ * d = 128), stops with PSA_ERR_TIMEOUT in its workspace status word, and later
+ * calls run normally.  Errors: PSA_ERR_ARG.
+ */
+PSA_API int psa_test_stall_next_serve(int on);
+
+/*
  * Synchronises `stream`, then copies the device status word of `workspace`
  * into *status (host pointer): PSA_OK, or the first device-side error
  * recorded since the last call that reset it (the routers, psa_attn and
