@@ -248,8 +248,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // others, since every CTA between a unit's first and its last one
         // writes that unit's parts
         int tile_sum = 0, unit_sum = 0;
+        const int front = sa + lane < sb ? seg_len(p, sa + lane) : 0;  // of its first 32 segments
         for (int s = sa + lane; s < sb; s += 32) {
-          const int len = seg_len(p, s);
+          const int len = s == sa + lane ? front : seg_len(p, s);
           tile_sum += seg_work(p, s, len, 0);
           unit_sum += len > 0 ? p.Hkv * (line ? p.own_up : p.pre_up) : 0;
         }
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the segment in which it starts, and that segment's place
         int lens0 = sa, lens = 0, off = 0, s = sa;  // lane l holds the length of segment lens0 + l
         for (;; lens0 += 32) {
-          lens = lens0 + lane < sb ? seg_len(p, lens0 + lane) : 0;
+          lens = lens0 == sa ? front : (lens0 + lane < sb ? seg_len(p, lens0 + lane) : 0);
           const int w = lens0 + lane < sb ? seg_work(p, lens0 + lane, lens, pad) : 0;
           int inc = w;
 #pragma unroll
@@ -460,6 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
         return mbar_sleep_warp(bar, parity, abort_flag, p.status);
       };
+      bool held = p.stall && blockIdx.x == 0;  // the test hook's first hand-off
       int np = 0, cnt = 0;         // pieces read, items issued
       int t = 0;                   // running key tile
       // the PV products due, of the items cnt - 2 and cnt - 1: tile and
@@ -529,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int kk = 0; kk < D / 16; ++kk)
               tc_mma_bf16(ds, a + (kk >> 2) * 1024 + (kk & 3) * 2, b + (kk >> 2) * 1024 + (kk & 3) * 2, kIdescS,
                           kk ? 1u : 0u);
-            if (!(p.stall && blockIdx.x == 0 && cnt == 0)) tc_commit(&s_full[s]);
+            if (!held) tc_commit(&s_full[s]);
             if (tile_end) tc_commit(&k_empty[st]);
             if (i >= ni - 1 - pair) tc_commit(&q_empty[qs]);
           }
@@ -540,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           t1 = t;
           f1 = (i >= 2 ? 1u : 0u) | (tile_end ? 2u : 0u) | (i >= ni - 2 ? 4u : 0u);
           ++cnt;
+          held = false;
           t += tile_end;
         }
       }
