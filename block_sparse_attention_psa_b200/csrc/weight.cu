@@ -15,8 +15,8 @@
 //
 //  * Decode reads K once for few queries: bound by DRAM.  A prefill does 2 d
 //    operations and one exponential per (query, key) pair: an SM's tensor
-//    core takes 256 cycles for a tile, its 16 exponentials a cycle 1024, so
-//    it is bound by the exponentials.
+//    core takes 256 cycles for a tile at d = 64 and 512 at d = 128, its 16
+//    exponentials a cycle 1024, so it is bound by the exponentials.
 //  * Up to 32 queries per key (16 at d = 128; decode): stream_kernel. 16 keys x 8 queries per
 //    mma.sync, with K going from DRAM straight to registers: a thread's four
 //    16-byte pieces of two key rows are its A operands, in an order of the d
@@ -43,7 +43,7 @@
 //    (fewest keys hidden) first.  Where that leaves the last SM at work for longer
 //    the query tiles of a unit are split over several (make_plan), whose sums a
 //    second kernel adds in a fixed order.
-//  * One in eight exponentials runs on the FMA pipe (exp2_parts, 7.5e-8), whose
+//  * One in eight exponentials runs on the FMA pipe (exp2_parts, 2.1e-7), whose
 //    other work leaves it half idle (8K prefill 354 -> 349 us, 64-token window
 //    121 -> 114; two in eight 348 and 117, three 380 and 127: the chains of
 //    the polynomial then cost more than the unit is relieved of).
@@ -230,7 +230,7 @@ __device__ __forceinline__ void sum32(const float (&v)[32], const float* nl, flo
     const int k = (i / 4) % 4;
     if (k < kPoly) {
       float p0, p1, s0, s1;
-      exp2_parts<5>(x2, x3, p0, p1, s0, s1);
+      exp2_parts(x2, x3, p0, p1, s0, s1);
       ffma2(a[2], a[3], p0, p1, s0, s1, a[2], a[3]);
     } else {
       fadd2(a[2], a[3], a[2], a[3], ex2_approx(x2), ex2_approx(x3));
