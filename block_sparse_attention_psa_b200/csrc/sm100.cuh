@@ -153,9 +153,11 @@ __device__ __forceinline__ bool named_barrier_or(int id, int nthreads, bool p) {
 // and its writes are visible (at once for a plain launch).  Because every
 // kernel of a chain waits this way, the wait also covers the grids further
 // back.  What the grids before may have written is then read by plain (or
-// __ldcg, __ldcs) loads, never by __ldg or through a const __restrict__ pointer: the
-// non-coherent path is defined for data that nothing writes while the kernel
-// lives, and it lives from before the wait.
+// __ldcg, __ldcs) loads, not by __ldg or through a const __restrict__ pointer:
+// the non-coherent path is defined for data that nothing writes while the
+// kernel lives, and it lives from before the wait.  (The serving kernels keep
+// to that; those of the prefill still read their lists, scores and pooled
+// means by __ldg.)
 // grid_dep_launch() lets the next launch of the stream be scheduled
 // as soon as every CTA of this grid has called it (or exited); a kernel that
 // holds tensor memory calls it only after its allocation has succeeded, so a
