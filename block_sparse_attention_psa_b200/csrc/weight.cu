@@ -760,8 +760,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ few queries
 // Queries per key set and KV head, at most.  32 caches of 4096, 8 KV heads, us a call,
-// this kernel against weight_kernel: d = 64: 12 rows 19 / 37, 28 rows 28 / 37;
-// d = 128: 12 rows 32 / 42, 20 rows 50 / 42.
+// this kernel against weight_kernel: d = 64: 12 rows 20 / 37, 28 rows 29 / 37;
+// d = 128: 12 rows 30 / 42, 20 rows 50 / 42.
 template <int D>
 constexpr int kStreamRows = D == 64 ? 32 : 16;
 constexpr int kStreamThreads = 256;
@@ -807,9 +807,9 @@ __global__ void __launch_bounds__(kStreamThreads, NT == 4 ? 1 : (D == 64 ? 3 : 2
   const int end = min(c0 + chunk, p.C);
   const long long base = static_cast<long long>(bh) * p.C;
   const uint4* kb = k + base * (D / 8);
-  // K of the first step before anything else.  Each key is read once, past the
-  // other lines of L1 (evict first: 48 caches 24.0 us a call, 26.5 with plain
-  // loads and 28.2 from L2); queries and lse, which all warps read, by plain ones.
+  // K of the first step before anything else.  Each key is read once and evicted
+  // first (48 caches of one token 22.7 us, 24.4 with plain loads; 64 of 4096 at
+  // d = 128 51 and 55); queries and lse, which all warps read, by plain loads.
   uint4 cur[2][kP];
   float sin = 0.f;
   auto fetch = [&](int key0, uint4 (&f)[2][kP], float& si) {
@@ -830,28 +830,37 @@ __global__ void __launch_bounds__(kStreamThreads, NT == 4 ? 1 : (D == 64 ? 3 : 2
   float nl[NT][2];
   int lim[NT][2];
   const int rows = p.n * p.GT;
+  // (rows past the last one read that again: loads under no condition are all
+  // under way at once; 28 rows a key 31.6 -> 28.9 us)
+  auto row_at = [&](int r) -> long long {
+    r = min(r, rows - 1);
+    const int i = r / p.GT;
+    return (static_cast<long long>(bk * p.n + i) * p.Hkv + hkv) * p.GT + (r - i * p.GT);
+  };
+  float lq[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const int r = 8 * j + g;
-    const int i = r / p.GT, rr = r - i * p.GT;
-    const uint4* src = q + ((static_cast<long long>(bk * p.n + i) * p.Hkv + hkv) * p.GT + rr) * (D / 8);
+    const long long at = row_at(8 * j + g);
 #pragma unroll
-    for (int m = 0; m < kP; ++m) qf[j][m] = r < rows ? src[t + 4 * m] : make_uint4(0, 0, 0, 0);
+    for (int m = 0; m < kP; ++m) qf[j][m] = q[at * (D / 8) + t + 4 * m];
+    lq[j] = p.lse[at];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) nl[j][e] = p.lse[row_at(8 * j + 2 * t + e)];
+  }
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
     // a query without lse adds nothing, whatever it holds (NaN too)
-    if (r < rows && p.lse[(static_cast<long long>(bk * p.n + i) * p.Hkv + hkv) * p.GT + rr] == -INFINITY)
+    if (8 * j + g >= rows || lq[j] == -INFINITY)
 #pragma unroll
       for (int m = 0; m < kP; ++m) qf[j][m] = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int r2 = 8 * j + 2 * t + e;
-      const int i2 = r2 / p.GT, rr2 = r2 - i2 * p.GT;
-      float l = -INFINITY;
-      if (r2 < rows) l = p.lse[(static_cast<long long>(bk * p.n + i2) * p.Hkv + hkv) * p.GT + rr2];
       // a query that saw nothing (lse -inf) adds nothing, to keys of NaN or
       // infinities neither (0 of the query times such a key is NaN)
-      const bool none = l == -INFINITY;
-      nl[j][e] = none ? -INFINITY : -l * kLog2e;
-      lim[j][e] = none ? -1 : (p.causal ? len - p.T + rr2 % p.T : INT_MAX);
+      const int r = 8 * j + 2 * t + e;
+      const bool none = r >= rows || nl[j][e] == -INFINITY;
+      nl[j][e] = none ? -INFINITY : -nl[j][e] * kLog2e;
+      lim[j][e] = none ? -1 : (p.causal ? len - p.T + r % p.T : INT_MAX);
     }
   }
   for (; key0 < min(end, len); key0 += 16 * kWarps) {
