@@ -3,8 +3,8 @@
 // A call on a short cache takes 5 to 10 us on the device; reading nine tensors
 // through Python, two allocations and a foreign call with two dozen arguments
 // took 12 us of the host's time beside the 5 of the library. Here the accepted
-// call costs 2 to 4 (one short decode 17.8 -> 9.1 us a call, an eviction in
-// given buffers 15.4 -> 6.5): the arguments are read from the tensors themselves, the
+// call costs 2 to 4 (one short decode 17.8 -> 9.8 us a call, an eviction in
+// given buffers 15.4 -> 6.8): the arguments are read from the tensors themselves, the
 // outputs allocated and the C entry point called on the tensors' device and its
 // current stream.
 //

@@ -48,12 +48,15 @@
 //    121 -> 114; two in eight 348 and 117, three 380 and 127: the chains of
 //    the polynomial then cost more than the unit is relieved of).
 //  * Sums: 128 columns in four fp32 accumulators, tile sums added with a
-//    compensation term (a key of a long prefill sums 10^5 terms).
+//    compensation term (a key of a long prefill sums 10^5 terms). The terms
+//    inside a tile (32 in a row) and the parts of a split unit are added
+//    without one: the 8K prefill is off by 5.6e-7 relative to 64 bits, a plain
+//    fp32 form by 1.3e-7; the window and single tokens by 3e-8, as that is.
 // Measured on one B200 (device time): one token of 48 caches of up to 4099,
-// 8 KV heads of 3, d = 64: 24 us, 5.1 TB/s (floor 19 us: the reads of K; of 64
-// caches of 4096 at d = 128 55 us, 5.9 TB/s). Last
+// 8 KV heads of 3, d = 64: 23 us, 5.5 TB/s (floor 19 us: the reads of K; of 64
+// caches of up to 4096 at d = 128 51 us, 6.3 TB/s). Last
 // 64 queries of a 128K prefill, 8 KV heads of 4, d = 128: 108 us (60:
-// exponentials). A whole 8K causal prefill of 32 heads: 346 us, 795 TFLOP/s
+// exponentials). A whole 8K causal prefill of 32 heads: 345 us, 797 TFLOP/s
 // (floors: 238 exponentials alone, 166 tensor core). A tile of 128 x 128 x 2
 // takes 2350 cycles, 1800 of them sums (88% of the exponential unit), the rest
 // hand-overs between tiles, and 2100 of 6100 between units of two tiles.

@@ -527,7 +527,8 @@ def psa_decode(q, k_cache=None, v_cache=None, cache_len=None, k_prefix=None, v_p
     own cache [B, Hkv, C, d], in one softmax.  ``prefix_len`` [Bp] and
     ``cache_len`` [B] (int32, None: the capacity) are the valid lengths; the
     last T valid cache entries are the new tokens (query t sees slots below
-    cache_len - (T - 1 - t)).  Returns out and, if requested, lse (float32
+    cache_len - (T - 1 - t)).  Rows past a length may hold anything; the new
+    tokens' values must be finite.  Returns out and, if requested, lse (float32
     [B, Hq, T])."""
     if stream is not None:
         with _on_stream(stream, q):

@@ -381,7 +381,9 @@ PSA_API int psa_key_weight(const void* q, const void* k, const float* lse, const
  * Eviction: every (sequence, KV head) keeps nk = min(cache_len, budget)
  * entries.  Entries rank: protected ones first (pos < sink, or among the
  * `recent` latest positions: pos > max pos - recent), then by score
- * descending (NaN lowest), equal scores by slot ascending; the first nk stay.
+ * descending (NaN as -inf), equal scores by slot ascending; the first nk stay.
+ * (Positions may repeat or be negative; where more entries are protected than
+ * stay, the scores decide among those.)
  * Slots below nk whose entry stays keep it; the others, ascending, take the
  * staying entries of the slots from nk on, ascending.
  *   in:  k, v 16-bit [B,Hkv,C,d]; score float32 [B,Hkv,C]; pos int32
@@ -425,8 +427,9 @@ PSA_API int psa_test_stall_next_serve(int on);
 /*
  * Synchronises `stream`, then copies the device status word of `workspace`
  * into *status (host pointer): PSA_OK, or the first device-side error
- * recorded since the last call that reset it (the routers, psa_attn and
- * psa_dense reset it at their start).  Returns PSA_OK or PSA_ERR_CUDA.
+ * recorded since the last call that reset it (the routers, psa_attn,
+ * psa_dense and the serving operators reset it at their start).  Returns
+ * PSA_OK or PSA_ERR_CUDA.
  */
 PSA_API int psa_read_status(const void* workspace, int* status, void* stream);
 
