@@ -373,7 +373,7 @@ const char* psa_status_string(int status) {
   }
 }
 
-int psa_version(void) { return 300; }
+int psa_version(void) { return 301; }
 
 size_t psa_workspace_size(int B, int H, int N, int d) {
   if (check_shape(B, H, N, d, kBlock) != PSA_OK) return 0;
