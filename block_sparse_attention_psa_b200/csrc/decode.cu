@@ -45,7 +45,7 @@
 // 42 us (23): 22 us of streaming at the DRAM's rate, the rest is the schedule
 // (1.7), the first load (3), the last tile's chain (5), the imbalance of the
 // SMs (4) and the join (5). 64 sequences of 64 heads over a 128K prefix: 299 to
-// 311 us replayed, 340 to 357 as called in a long run, 770 to 920 TFLOP/s
+// 311 us replayed, 339 to 360 as called in a long run, 770 to 920 TFLOP/s
 // (166): a pair of items takes ~3280 cycles, set by
 // one stream's chain S -> softmax (2030: 128 exponentials of a thread alone are
 // 1024) -> PV -> S, the tensor core working 2048 of them, under the power cap
